@@ -12,6 +12,9 @@ without the built library, or without a CUDA device, raises.
 The recurrence ("Kimi Delta Attention 徹底解説" (tech-tide.dev), § "Kimi Delta
 Attention の仕組み"), per (sequence, head), with a dk x dv fp32 state S:
     S' = Diag(exp(log_alpha_t)) S;  S = S' + beta_t k_t (v_t - S'^T k_t)^T;  o_t = S^T q_t
+
+Linear attention with a constant decay for each head (la_*: S = exp(log_decay_h) S + k_t v_t^T)
+shares its layouts, states and slots; group_norm is the norm behind either kind of layer.
 """
 from __future__ import annotations
 
@@ -25,6 +28,9 @@ __all__ = [
     "chunk_forward", "chunk_backward", "gdn_chunk_backward", "backward_workspace_size", "chunk_forward_prologue",
     "recurrent_step_prologue", "chunk_forward_simt", "chunk_forward_static_ws", "chunk_forward_slots", "recurrent_step",
     "recurrent_step_slots", "gdn_chunk_forward", "gdn_recurrent_step", "workspace_size", "set_auto_workspace_limit",
+    "la_chunk_forward", "la_chunk_forward_slots", "la_chunk_backward", "la_recurrent_step", "la_recurrent_step_slots",
+    "la_workspace_size", "la_backward_workspace_size", "group_norm", "group_norm_backward", "group_norm_workspace_size",
+    "ACTIVATIONS",
     "device_status",
     "debug_wait_timeout", "last_error", "library_path", "load_library", "KDAError", "KDA_BF16", "KDA_F32", "CHUNK",
     "DEV_WAIT_TIMEOUT", "DEV_DECAY_RANGE", "DEV_BAD_SLOT", "ALGOS",
@@ -105,6 +111,27 @@ def load_library():
     lib.kda_chunk_backward_ex.restype = ci
     lib.kda_gdn_chunk_backward_ex.argtypes = lib.kda_chunk_backward_ex.argtypes
     lib.kda_gdn_chunk_backward_ex.restype = ci
+    lib.kda_la_chunk_forward_workspace_size.argtypes = [ci] * 8
+    lib.kda_la_chunk_forward_workspace_size.restype = sz
+    lib.kda_la_chunk_forward.argtypes = [vp] * 8 + [ci] * 7 + [vp, sz, vp]
+    lib.kda_la_chunk_forward.restype = ci
+    lib.kda_la_chunk_forward_slots.argtypes = [vp] * 8 + [ci] * 8 + [vp, sz, vp]
+    lib.kda_la_chunk_forward_slots.restype = ci
+    lib.kda_la_recurrent_step.argtypes = [vp] * 6 + [ci] * 5 + [vp]
+    lib.kda_la_recurrent_step.restype = ci
+    lib.kda_la_recurrent_step_slots.argtypes = [vp] * 7 + [ci] * 6 + [vp]
+    lib.kda_la_recurrent_step_slots.restype = ci
+    lib.kda_la_chunk_backward_workspace_size.argtypes = [ci] * 7
+    lib.kda_la_chunk_backward_workspace_size.restype = sz
+    lib.kda_la_chunk_backward.argtypes = [vp] * 12 + [ci] * 7 + [vp, sz, vp]
+    lib.kda_la_chunk_backward.restype = ci
+    ll, cf = ctypes.c_longlong, ctypes.c_float
+    lib.kda_group_norm_workspace_size.argtypes = [ll, ci, ci, ci, ci, ci]
+    lib.kda_group_norm_workspace_size.restype = sz
+    lib.kda_group_norm_forward.argtypes = [vp] * 7 + [ll, ci, ci, ci, cf, ci, ci, vp, sz, vp]
+    lib.kda_group_norm_forward.restype = ci
+    lib.kda_group_norm_backward.argtypes = [vp] * 11 + [ll, ci, ci, ci, ci, ci, vp, sz, vp]
+    lib.kda_group_norm_backward.restype = ci
     lib.kda_last_error.argtypes = []
     lib.kda_last_error.restype = ctypes.c_char_p
     lib.kda_get_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint), ci, vp]
@@ -507,6 +534,301 @@ def gdn_recurrent_step(q, k, v, log_alpha, beta, state, o=None):
                                                N, H, dk, dv, _dtype_code(q), _stream(q.device))
     _check(rc)
     return o
+
+
+# ---------------------------------------------------------------------------
+# linear attention with a decay for each head, and group norm
+#
+# These calls take CUDA tensors of one device (which need not be the current one) and
+# run on that device's current stream.
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _on_device(dev, **tensors):
+    """Every given tensor is a contiguous one on `dev`."""
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous in the documented layout")
+
+
+def _expect(name, t, shape, dtype):
+    if t is not None and (t.shape != shape or t.dtype != dtype):
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+
+
+def _call(dev, entry, *args):
+    """One library call on dev's current stream (the last argument)."""
+    if dev.index == torch.cuda.current_device():
+        rc = entry(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = entry(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if rc != 0:
+        raise KDAError(rc, last_error())
+
+
+def _scratch(workspace, need, dev):
+    """The workspace to pass and its bytes; allocated here unless given."""
+    if workspace is None:
+        return (torch.empty(need, dtype=torch.uint8, device=dev), need) if need else (None, 0)
+    _on_device(dev, workspace=workspace)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _la_shapes(q, k, v, log_decay, cu_seqlens):
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k and v must be [B, T, H, d]")
+    B, T, H, dk = q.shape
+    dv = v.shape[3]
+    dt = _dtype_code(q)
+    _expect("k", k, q.shape, q.dtype)
+    _expect("v", v, (B, T, H, dv), q.dtype)
+    _expect("log_decay", log_decay, (H,), torch.float32)
+    if cu_seqlens is None:
+        return B, T, H, dk, dv, B, dt
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or cu_seqlens.dtype != torch.int32:
+        raise ValueError("cu_seqlens must be int32 [num_seqs + 1]")
+    return B, T, H, dk, dv, cu_seqlens.shape[0] - 1, dt
+
+
+def la_workspace_size(B, T, H, dk, dv, num_seqs, dtype=torch.bfloat16, slots=False) -> int:
+    """Workspace bytes of la_chunk_forward (slots=True: of la_chunk_forward_slots)."""
+    code = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}[dtype]
+    return int(load_library().kda_la_chunk_forward_workspace_size(B, T, H, dk, dv, num_seqs, code, int(slots)))
+
+
+def la_backward_workspace_size(B, T, H, dk, dv, num_seqs, dtype=torch.bfloat16) -> int:
+    """Workspace bytes of la_chunk_backward."""
+    code = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}[dtype]
+    return int(load_library().kda_la_chunk_backward_workspace_size(B, T, H, dk, dv, num_seqs, code))
+
+
+def la_chunk_forward(q, k, v, log_decay, init_state=None, cu_seqlens=None, *, o=None, final_state=True,
+                     workspace=None):
+    """Linear attention with a decay for each head over whole prompts (kda_la_chunk_forward):
+    S = exp(log_decay_h) S + k_t v_t^T, o_t = S^T q_t.
+
+    Tensors are in the include/kda.h layouts, log_decay is float32 [H].  `final_state` may be
+    True (allocate and return), False (skip) or a preallocated float32 tensor; the workspace
+    (uint8, la_workspace_size bytes) is allocated here unless given.
+    Returns (o, final_state or None).
+    """
+    B, T, H, dk, dv, N, dt = _la_shapes(q, k, v, log_decay, cu_seqlens)
+    dev = q.device
+    _expect("init_state", init_state, (N, H, dk, dv), torch.float32)
+    if o is None:
+        o = torch.empty_like(v)
+    else:
+        _expect("o", o, v.shape, q.dtype)
+    if final_state is True:
+        final_state = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+    elif final_state is False:
+        final_state = None
+    else:
+        _expect("final_state", final_state, (N, H, dk, dv), torch.float32)
+    _on_device(dev, q=q, k=k, v=v, log_decay=log_decay, init_state=init_state, cu_seqlens=cu_seqlens, o=o,
+               final_state=final_state)
+    lib = load_library()
+    ws, nb = _scratch(workspace, lib.kda_la_chunk_forward_workspace_size(B, T, H, dk, dv, N, dt, 0), dev)
+    _call(dev, lib.kda_la_chunk_forward, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+          _ptr(init_state), o.data_ptr(), _ptr(final_state), _ptr(cu_seqlens), B, T, H, dk, dv, N, dt, _ptr(ws), nb)
+    return o, final_state
+
+
+def la_chunk_forward_slots(q, k, v, log_decay, state_pool, slots, cu_seqlens=None, *, o=None, workspace=None):
+    """la_chunk_forward from and into a state pool (kda_la_chunk_forward_slots): sequence n
+    starts from state_pool[slots[n]] and its final state is written back there (slot -1:
+    start from zeros, write nothing).  Returns o."""
+    B, T, H, dk, dv, N, dt = _la_shapes(q, k, v, log_decay, cu_seqlens)
+    dev = q.device
+    _expect("state_pool", state_pool, (*state_pool.shape[:1], H, dk, dv), torch.float32)
+    _expect("slots", slots, (N,), torch.int32)
+    if o is None:
+        o = torch.empty_like(v)
+    else:
+        _expect("o", o, v.shape, q.dtype)
+    _on_device(dev, q=q, k=k, v=v, log_decay=log_decay, state_pool=state_pool, slots=slots, cu_seqlens=cu_seqlens,
+               o=o)
+    lib = load_library()
+    ws, nb = _scratch(workspace, lib.kda_la_chunk_forward_workspace_size(B, T, H, dk, dv, N, dt, 1), dev)
+    _call(dev, lib.kda_la_chunk_forward_slots, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+          state_pool.data_ptr(), slots.data_ptr(), o.data_ptr(), _ptr(cu_seqlens), B, T, H, dk, dv, N,
+          state_pool.shape[0], dt, _ptr(ws), nb)
+    return o
+
+
+def la_chunk_backward(q, k, v, log_decay, d_o, init_state=None, dfinal_state=None, cu_seqlens=None, *,
+                      dinit_state=True, workspace=None, out=None):
+    """Gradients of sum <d_o, o> + <dfinal_state, final_state> through la_chunk_forward
+    (kda_la_chunk_backward): a dict with dq, dk, dv (in q's dtype) and dinit_state (float32;
+    None when dinit_state=False).  The rates are constants: log_decay has no gradient.
+
+    d_o has o's shape and dtype, dfinal_state is float32 [N, H, dk, dv] or None (zero).  The
+    workspace and the outputs (`out`, a dict with any of the keys) are allocated here unless given.
+    """
+    B, T, H, dk, dv, N, dt = _la_shapes(q, k, v, log_decay, cu_seqlens)
+    dev = q.device
+    state = (N, H, dk, dv)
+    _expect("init_state", init_state, state, torch.float32)
+    _expect("d_o", d_o, v.shape, q.dtype)
+    _expect("dfinal_state", dfinal_state, state, torch.float32)
+    g = dict(out or {})
+    for name, like in (("dq", q), ("dk", k), ("dv", v)):
+        if g.get(name) is None:
+            g[name] = torch.empty_like(like)
+        else:
+            _expect(name, g[name], like.shape, like.dtype)
+    if not dinit_state:
+        g["dinit_state"] = None
+    elif g.get("dinit_state") is None:
+        g["dinit_state"] = torch.empty(state, dtype=torch.float32, device=dev)
+    else:
+        _expect("dinit_state", g["dinit_state"], state, torch.float32)
+    _on_device(dev, q=q, k=k, v=v, log_decay=log_decay, init_state=init_state, d_o=d_o, dfinal_state=dfinal_state,
+               cu_seqlens=cu_seqlens, **g)
+    lib = load_library()
+    ws, nb = _scratch(workspace, lib.kda_la_chunk_backward_workspace_size(B, T, H, dk, dv, N, dt), dev)
+    _call(dev, lib.kda_la_chunk_backward, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+          _ptr(init_state), d_o.data_ptr(), _ptr(dfinal_state), g["dq"].data_ptr(), g["dk"].data_ptr(),
+          g["dv"].data_ptr(), _ptr(g["dinit_state"]), _ptr(cu_seqlens), B, T, H, dk, dv, N, dt, _ptr(ws), nb)
+    return g
+
+
+def _la_step_shapes(q, k, v, log_decay):
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v must be [N, H, d]")
+    N, H, dk = q.shape
+    dv = v.shape[2]
+    dt = _dtype_code(q)
+    _expect("k", k, q.shape, q.dtype)
+    _expect("v", v, (N, H, dv), q.dtype)
+    _expect("log_decay", log_decay, (H,), torch.float32)
+    return N, H, dk, dv, dt
+
+
+def la_recurrent_step(q, k, v, log_decay, state, o=None):
+    """One token of linear attention with a decay for each head (kda_la_recurrent_step);
+    `state` [N, H, dk, dv] float32 is updated in place.  Returns o."""
+    N, H, dk, dv, dt = _la_step_shapes(q, k, v, log_decay)
+    dev = q.device
+    _expect("state", state, (N, H, dk, dv), torch.float32)
+    if o is None:
+        o = torch.empty_like(v)
+    else:
+        _expect("o", o, v.shape, q.dtype)
+    _on_device(dev, q=q, k=k, v=v, log_decay=log_decay, state=state, o=o)
+    _call(dev, load_library().kda_la_recurrent_step, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+          state.data_ptr(), o.data_ptr(), N, H, dk, dv, dt)
+    return o
+
+
+def la_recurrent_step_slots(q, k, v, log_decay, state_pool, slots, o=None):
+    """la_recurrent_step on a state pool (kda_la_recurrent_step_slots): sequence n uses and
+    updates state_pool[slots[n]] in place (slot -1: padding, o row zero).  Returns o."""
+    N, H, dk, dv, dt = _la_step_shapes(q, k, v, log_decay)
+    dev = q.device
+    _expect("state_pool", state_pool, (*state_pool.shape[:1], H, dk, dv), torch.float32)
+    _expect("slots", slots, (N,), torch.int32)
+    if o is None:
+        o = torch.empty_like(v)
+    else:
+        _expect("o", o, v.shape, q.dtype)
+    _on_device(dev, q=q, k=k, v=v, log_decay=log_decay, state_pool=state_pool, slots=slots, o=o)
+    _call(dev, load_library().kda_la_recurrent_step_slots, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          log_decay.data_ptr(), state_pool.data_ptr(), slots.data_ptr(), o.data_ptr(), N, H, dk, dv,
+          state_pool.shape[0], dt)
+    return o
+
+
+ACTIVATIONS = {"none": 0, "silu": 1, "sigmoid": 2}   # KDA_ACT_*
+
+
+def _norm_shapes(x, num_groups, weight, bias, gate, activation):
+    if x.dim() < 2:
+        raise ValueError("x must be [N, ..., C], channels last")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
+    N, C = x.shape[0], x.shape[-1]
+    L = 1
+    for n in x.shape[1:-1]:
+        L *= n
+    if num_groups < 1 or C % num_groups:
+        raise ValueError(f"{C} channels do not divide into {num_groups} groups")
+    if L < 1 or C < 1:
+        raise ValueError("a sample must hold at least one position and one channel")
+    _expect("weight", weight, (C,), torch.float32)
+    _expect("bias", bias, (C,), torch.float32)
+    _expect("gate", gate, x.shape, x.dtype)
+    return N, L, C, _dtype_code(x), ACTIVATIONS[activation]
+
+
+def group_norm_workspace_size(N, L, C, num_groups, dtype=torch.bfloat16, backward=False) -> int:
+    """Workspace bytes of group_norm (or of group_norm_backward) for x [N, L positions, C]."""
+    code = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}[dtype]
+    return int(load_library().kda_group_norm_workspace_size(N, L, C, num_groups, code, int(backward)))
+
+
+def group_norm(x, num_groups, weight=None, bias=None, gate=None, *, eps=1e-5, activation="silu", y=None,
+               workspace=None):
+    """Group norm with an activation, channels last (kda_group_norm_forward): each sample's
+    `num_groups` groups of channels are normalised over their channels and all positions,
+    z = xhat * weight + bias, and y = act(z), or z * act(gate) with a gate.
+
+    x and gate are [N, ..., C] (the axes between are positions; [N, C]: one position, e.g.
+    the heads of an attention output viewed as [B T, H dv] with num_groups = H), weight and
+    bias float32 [C].  Returns (y, mean, rstd), the statistics float32 [N, num_groups].
+    """
+    N, L, C, dt, act = _norm_shapes(x, num_groups, weight, bias, gate, activation)
+    if not eps > 0:
+        raise ValueError(f"eps must be above 0, got {eps}")
+    dev = x.device
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _expect("y", y, x.shape, x.dtype)
+    _on_device(dev, x=x, weight=weight, bias=bias, gate=gate, y=y)
+    mean = torch.empty((N, num_groups), dtype=torch.float32, device=dev)
+    rstd = torch.empty((N, num_groups), dtype=torch.float32, device=dev)
+    lib = load_library()
+    ws, nb = _scratch(workspace, lib.kda_group_norm_workspace_size(N, L, C, num_groups, dt, 0), dev)
+    _call(dev, lib.kda_group_norm_forward, x.data_ptr(), _ptr(weight), _ptr(bias), _ptr(gate), y.data_ptr(),
+          mean.data_ptr(), rstd.data_ptr(), N, L, C, num_groups, eps, act, dt, _ptr(ws), nb)
+    return y, mean, rstd
+
+
+def group_norm_backward(dy, x, mean, rstd, num_groups, weight=None, bias=None, gate=None, *, activation="silu",
+                        out=None, workspace=None):
+    """Gradients of sum <dy, y> through group_norm (kda_group_norm_backward): a dict with dx,
+    dweight and dbias (float32, when weight, bias are given) and dgate (with a gate).
+    `mean` and `rstd` are what group_norm returned; `out` may hold any of the outputs."""
+    N, L, C, dt, act = _norm_shapes(x, num_groups, weight, bias, gate, activation)
+    dev = x.device
+    _expect("dy", dy, x.shape, x.dtype)
+    _expect("mean", mean, (N, num_groups), torch.float32)
+    _expect("rstd", rstd, (N, num_groups), torch.float32)
+    g = dict(out or {})
+    for name, like in (("dx", x), ("dgate", gate), ("dweight", weight), ("dbias", bias)):
+        if like is None:
+            g.pop(name, None)
+        elif g.get(name) is None:
+            g[name] = torch.empty_like(like)
+        else:
+            _expect(name, g[name], like.shape, like.dtype)
+    _on_device(dev, dy=dy, x=x, mean=mean, rstd=rstd, weight=weight, bias=bias, gate=gate, **g)
+    lib = load_library()
+    ws, nb = _scratch(workspace, lib.kda_group_norm_workspace_size(N, L, C, num_groups, dt, 1), dev)
+    _call(dev, lib.kda_group_norm_backward, dy.data_ptr(), x.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+          _ptr(weight), _ptr(bias), _ptr(gate), g["dx"].data_ptr(), _ptr(g.get("dgate")), _ptr(g.get("dweight")),
+          _ptr(g.get("dbias")), N, L, C, num_groups, act, dt, _ptr(ws), nb)
+    return g
 
 
 def debug_wait_timeout(limit_cycles: int = 2_000_000) -> None:

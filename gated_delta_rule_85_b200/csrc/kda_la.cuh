@@ -1,0 +1,203 @@
+// Linear attention with a decay for each head: what its kernels share.
+//
+// Per (sequence, head), with g = exp(log_decay_h), one constant rate per head:
+//   S_t = g S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t                       (S: dk x dv, fp32)
+// A chunk of L tokens that starts from state S (0-based i, j):
+//   o_i = g^{i+1} S^T q_i + sum_{j<=i} g^{i-j} (q_i . k_j) v_j
+//   S'  = g^L S + sum_j g^{L-1-j} k_j v_j^T
+// The backward pass has the same form.  With X = g (adjoint of the state at the next
+// chunk's first token), and X = dL/dfinal_state behind the last token:
+//   dq_i = g^{i+1} S do_i       + sum_{j<=i} g^{i-j} (do_i . v_j) k_j
+//   dk_i = g^{L-1-i} X v_i      + sum_{j>=i} g^{j-i} (v_i . do_j) q_j
+//   dv_i = g^{L-1-i} X^T k_i    + sum_{j>=i} g^{j-i} (k_i . q_j) do_j
+//   X'   = g^L X + sum_j g^{j+1} q_j do_j^T,   dL/dinit_state = X at the first token
+// So one walk, in either direction, computes all of them: rows a attend to rows b
+// and sum rows c, out_i = u_i S^T a_i + sum_j g^|i-j| (a_i . b_j) c_j with the state
+// summing b c^T:
+//   forward (a, b, c) = (q, k, v);  dq (do, v, k) on S^T;  backwards in time
+//   dk (v, do, q) on X^T and dv (k, q, do) on X.
+//
+// Work split: the (head, chunk) items of a call are laid out head by head and cut
+// into W equal spans, one per CTA, so that every SM gets the same share whatever the
+// lengths.  A span may start or end inside a sequence; a first pass sums b c^T over
+// the part of each cut sequence that lies in a span, a small scan joins those sums
+// into the state every span starts from, and the walk then runs each span from there.
+#pragma once
+
+#include <algorithm>
+
+#include "kda_common.cuh"
+
+namespace kda {
+namespace la {
+
+constexpr int kSMs = 148;
+
+// Token geometry of one call.  Chunks of C tokens are counted from each sequence's
+// start; chunk c of sequence n has slot f(n) + c, f(n) = floor(t0 / C) + n for packed
+// input (unique, below floor(T / C) + N, with holes) and n ceil(T / C) for a dense batch.
+struct Geo {
+    const int32_t *cu;   // packed offsets, or null
+    int T, N, H;         // tokens of a row (packed: of the call), sequences, heads
+    int nslots;          // chunk slots of one head
+    int W;               // spans
+    __host__ __device__ long long items() const { return (long long)H * nslots; }
+    __host__ __device__ long long lo(int w) const { return items() * w / W; }
+    __host__ __device__ long long hi(int w) const { return items() * (w + 1) / W; }
+};
+
+// Where one item lies.  seek and step are warp-collective (all 32 lanes, converged).
+template <int C>
+struct Cursor {
+    long long t0, t1;    // the sequence's tokens
+    int h, n, c, nck;    // head, sequence, chunk and number of chunks of the sequence
+    int slot;
+    bool valid;          // false: a hole between packed sequences
+
+    __device__ __forceinline__ static int first_slot(const Geo &g, int n) {
+        return min(max(g.cu[n], 0), g.T) / C + n;
+    }
+
+    __device__ void seek(const Geo &g, long long u) {
+        h = (int)(u / g.nslots);
+        slot = (int)(u - (long long)h * g.nslots);
+        if (!g.cu) {
+            nck = (g.T + C - 1) / C;
+            n = slot / nck;
+            c = slot - n * nck;
+            t0 = (long long)n * g.T;
+            t1 = t0 + g.T;
+            valid = true;
+            return;
+        }
+        // the last sequence whose first slot is not behind this one: a 32-way search
+        const int lane = threadIdx.x & 31;
+        int a = 0, b = g.N;
+        valid = false;
+        while (true) {
+            const int step = max(1, (b - a + 31) / 32);
+            const int m = a + lane * step;
+            const unsigned hit = __ballot_sync(0xffffffffu, m < b && first_slot(g, m) <= slot);
+            const int cnt = hit == 0xffffffffu ? 32 : __ffs(~hit) - 1;
+            if (cnt == 0) return;
+            a += (cnt - 1) * step;
+            if (step == 1) break;
+            b = min(b, a + step);
+        }
+        n = a;
+        seq_span(g.cu, g.T, n, t0, t1);
+        c = slot - first_slot(g, n);
+        nck = (int)((t1 - t0 + C - 1) / C);
+        valid = c >= 0 && c < nck;
+    }
+
+    // From the item u - DIR to the item u.
+    template <int DIR>
+    __device__ __forceinline__ void step(const Geo &g, long long u) {
+        if (valid && c + DIR >= 0 && c + DIR < nck) {
+            c += DIR;
+            slot += DIR;
+        } else {
+            seek(g, u);
+        }
+    }
+    __device__ __forceinline__ long long tok() const { return t0 + (long long)c * C; }
+    __device__ __forceinline__ int len() const { return (int)min((long long)C, t1 - tok()); }
+};
+
+// exp(log_decay e) with the exponent's product in 64 bits, as the sum of two floats:
+// a chunk's decay is applied once per chunk of a sequence, so an error in its last
+// place would grow with the number of chunks.
+__device__ __forceinline__ float2 decay2(float log_decay, double e) {
+    const double x = exp((double)log_decay * e);
+    const float hi = (float)x;
+    return make_float2(hi, (float)(x - (double)hi));
+}
+
+// One set of states that the spans hand on: sums of the cut parts and start states.
+struct Carry {
+    float *sum_in;       // [W][dk dv] the part that comes from the span before (in walking order)
+    float *sum_out;      // [W][dk dv] the part that starts in the span and goes on behind it
+    float *start;        // [W][dk dv] the state at the span's first item
+    const float *s0;     // initial states [rows][H][dk dv] or null (zeros)
+    float *s0_copy;      // [N][H][dk dv]: s0 as read, kept when `last` overwrites it; or null
+    float *last;         // final states [rows][H][dk dv] or null
+};
+
+// Joins the cut parts: thread = four elements of the state; CTA column w (blockIdx.x < W)
+// follows the sequence that goes on behind span w from span to span.  The sums are
+// independent loads, fetched kAhead spans ahead of the recurrence that adds them up.
+// WANT_LAST: the part in the span where the sequence ends has a sum too, and `last` is
+// written here; without it the walk writes it.  Columns W.. (packed): one sequence each,
+// handed through when it has no tokens.
+template <int C, int DIR, bool WANT_LAST>
+__global__ void __launch_bounds__(256) la_join_kernel(Geo g, Carry y, const float *__restrict__ log_decay, int E,
+                                                      const int32_t *__restrict__ slots, int num_slots) {
+    const int e = (blockIdx.y * 256 + threadIdx.x) * 4;   // E is a multiple of 1024
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    if ((int)blockIdx.x >= g.W) {
+        const int n = blockIdx.x - g.W;
+        long long t0, t1;
+        seq_span(g.cu, g.T, n, t0, t1);
+        const int row = state_row(slots, num_slots, n);
+        if (t1 > t0 || !y.last || y.last == y.s0 || row < 0) return;
+        for (int h = 0; h < g.H; ++h) {
+            const long long off = ((long long)row * g.H + h) * E + e;
+            store4(y.last + off, y.s0 ? load4(y.s0 + off) : zero);
+        }
+        return;
+    }
+    int w = blockIdx.x;
+    const long long lo = g.lo(w), hi = g.hi(w);
+    Cursor<C> cur;
+    const long long edge = DIR > 0 ? hi - 1 : lo;
+    cur.seek(g, edge);
+    // the sequence at the span's far edge must start inside the span and go on behind it
+    if (!cur.valid || cur.c == (DIR > 0 ? cur.nck - 1 : 0)) return;
+    const long long u_first = DIR > 0 ? edge - cur.c : edge + (cur.nck - 1 - cur.c);
+    if (DIR > 0 ? u_first < lo : u_first >= hi) return;
+    const long long u_last = DIR > 0 ? u_first + cur.nck - 1 : u_first - (cur.nck - 1);
+    const float lg = log_decay[cur.h];
+    const int row = state_row(slots, num_slots, cur.n);
+    const long long off = ((long long)max(row, 0) * g.H + cur.h) * E + e;
+    const float4 s0 = row >= 0 && y.s0 ? load4(y.s0 + off) : zero;
+    if (y.s0_copy) store4(y.s0_copy + ((long long)cur.n * g.H + cur.h) * E + e, s0);
+    auto add = [](float2 d, float4 s, float4 u) {
+        return make_float4(fmaf(d.x, s.x, fmaf(d.y, s.x, u.x)), fmaf(d.x, s.y, fmaf(d.y, s.y, u.y)),
+                           fmaf(d.x, s.z, fmaf(d.y, s.z, u.z)), fmaf(d.x, s.w, fmaf(d.y, s.w, u.w)));
+    };
+    const long long begun = DIR > 0 ? (long long)(cur.c + 1) * C : cur.t1 - cur.tok();   // tokens so far
+    float4 s = add(decay2(lg, (double)begun), s0, load4(y.sum_out + (long long)w * E + e));
+    w += DIR;
+    store4(y.start + (long long)w * E + e, s);
+    // spans that the sequence crosses from edge to edge, then the one it ends in
+    constexpr int kAhead = 8;
+    auto crossed = [&](int x) { return DIR > 0 ? u_last >= g.hi(x) : u_last < g.lo(x); };
+    while (crossed(w)) {
+        float4 u[kAhead];
+        int m = 0;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int x = w + i * DIR;
+            if (m == i && x >= 0 && x < g.W && crossed(x)) {
+                u[i] = load4(y.sum_in + (long long)x * E + e);
+                m = i + 1;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (i < m) {
+                s = add(decay2(lg, (double)(g.hi(w) - g.lo(w)) * C), s, u[i]);
+                w += DIR;
+                store4(y.start + (long long)w * E + e, s);
+            }
+    }
+    if (WANT_LAST && y.last && row >= 0) {
+        const long long left = DIR > 0 ? cur.t1 - (cur.t0 + (g.lo(w) - u_first) * C)
+                                       : (g.hi(w) - u_last) * (long long)C;
+        store4(y.last + off, add(decay2(lg, (double)left), s, load4(y.sum_in + (long long)w * E + e)));
+    }
+}
+
+}  // namespace la
+}  // namespace kda

@@ -1,0 +1,88 @@
+// Linear attention with a decay for each head, one token per (sequence, head):
+//   S = g S + k v^T,  o = S^T q,   g = exp(log_decay_h)
+// The dk x dv fp32 state is read once and written once.
+//
+// Mapping: one 256-thread CTA per (n, h), as in the delta-rule decode step: warp w owns
+// a 32-column stripe and a group of rows, lane l four consecutive columns of every
+// fourth row; the sum over the key axis runs in registers, across the warp's four row
+// lanes by shuffles, then across the row groups through shared memory.
+#pragma once
+
+#include "kda_common.cuh"
+
+namespace kda {
+namespace la {
+
+template <int DK, int DV, typename Tin>
+__global__ void __launch_bounds__(256, 2)
+la_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin *__restrict__ v,
+               const float *__restrict__ log_decay, float *__restrict__ state, Tin *__restrict__ o,
+               const int32_t *__restrict__ slots, int num_slots, int H) {
+    constexpr int NSTRIPE = DV / 32;
+    constexpr int RG = 8 / NSTRIPE;          // row groups (warps of a stripe)
+    constexpr int RPT = DK / RG / 4;         // rows of a thread
+    const long long pair = blockIdx.x;       // n H + h
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int stripe = warp % NSTRIPE, rg = warp / NSTRIPE;
+    const int rl = lane >> 3;
+    const int col0 = stripe * 32 + (lane & 7) * 4;
+    const int row0 = rg * (DK / RG) + rl;    // this thread's rows: row0 + 4 m
+
+    __shared__ float s_k[DK], s_q[DK];
+    __shared__ float4 s_red[RG][DV / 4];
+
+    const int row = state_row(slots, num_slots, (int)(pair / H));
+    const int h = (int)(pair % H);
+    if (row < 0) {   // padding: its output row is zero
+        if (rg == 0 && rl == 0) store4(o + pair * DV + col0, make_float4(0.f, 0.f, 0.f, 0.f));
+        return;
+    }
+    float *S = state + ((long long)row * H + h) * (long long)(DK * DV);
+    float4 s[RPT];   // every load of the state in flight first
+#pragma unroll
+    for (int m = 0; m < RPT; ++m) s[m] = ld_stream(S + (row0 + 4 * m) * DV + col0);
+    if (tid < DK) s_k[tid] = Elem<Tin>::load(k + pair * DK + tid);
+    else if (tid < 2 * DK) s_q[tid - DK] = Elem<Tin>::load(q + pair * DK + tid - DK);
+    const float4 vv = load4(v + pair * DV + col0);
+    const float g = expf(log_decay[h]);
+    __syncthreads();
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int m = 0; m < RPT; ++m) {
+        const int c = row0 + 4 * m;
+        const float kc = s_k[c], qc = s_q[c];
+        float4 x;
+        x.x = fmaf(g, s[m].x, kc * vv.x);
+        x.y = fmaf(g, s[m].y, kc * vv.y);
+        x.z = fmaf(g, s[m].z, kc * vv.z);
+        x.w = fmaf(g, s[m].w, kc * vv.w);
+        st_stream(S + c * DV + col0, x);
+        acc.x = fmaf(qc, x.x, acc.x);
+        acc.y = fmaf(qc, x.y, acc.y);
+        acc.z = fmaf(qc, x.z, acc.z);
+        acc.w = fmaf(qc, x.w, acc.w);
+    }
+#pragma unroll
+    for (int off = 8; off <= 16; off <<= 1) {
+        acc.x += __shfl_xor_sync(0xffffffffu, acc.x, off);
+        acc.y += __shfl_xor_sync(0xffffffffu, acc.y, off);
+        acc.z += __shfl_xor_sync(0xffffffffu, acc.z, off);
+        acc.w += __shfl_xor_sync(0xffffffffu, acc.w, off);
+    }
+    if (rl == 0) s_red[rg][col0 / 4] = acc;
+    __syncthreads();
+    if (tid < DV / 4) {
+        float4 r = s_red[0][tid];
+#pragma unroll
+        for (int x = 1; x < RG; ++x) {
+            r.x += s_red[x][tid].x;
+            r.y += s_red[x][tid].y;
+            r.z += s_red[x][tid].z;
+            r.w += s_red[x][tid].w;
+        }
+        store4(o + pair * DV + tid * 4, r);
+    }
+}
+
+}  // namespace la
+}  // namespace kda

@@ -14,6 +14,10 @@
 #include "kda_chunk_2pass.cuh"
 #include "kda_bwd_simt.cuh"
 #include "kda_bwd_tc.cuh"
+#include "kda_la.cuh"
+#include "kda_la_simt.cuh"
+#include "kda_la_step.cuh"
+#include "kda_norm.cuh"
 
 namespace {
 
@@ -476,6 +480,99 @@ int backward_impl(const void *q, const void *k, const void *v, const float *log_
 #undef KDA_BWD_ARGS
 }
 
+// ------------------------------------------------------------------ linear attention with a decay for each head
+
+// Shared checks of the prefill and its backward pass; `states` names two optional fp32 state tensors.
+int check_la(const void *q, const void *k, const void *v, const float *log_decay, const float *s0, const void *o,
+             const float *last, const int32_t *cu_seqlens, int B, int T, int H, int dk, int dv, int num_seqs, int dtype) {
+    // beta is not part of this operator: log_decay stands in (both are 4-byte aligned device arrays)
+    int rc = check_prefill(q, k, v, log_decay, log_decay, s0, o, last, cu_seqlens, B, T, H, dk, dv, num_seqs, dtype, 64,
+                           true);
+    if (rc) return rc;
+    if ((long long)B * T > 0x7fffffffLL)
+        return fail(KDA_ERR_UNSUPPORTED, "B*T=%lld exceeds 2^31 - 1 tokens", (long long)B * T);
+    return KDA_OK;
+}
+
+int check_workspace(const void *workspace, size_t ws_bytes, size_t need) {
+    if (need && (!workspace || ws_bytes < need))
+        return fail(KDA_ERR_WORKSPACE, "workspace of %zu bytes required, got %zu%s", need, ws_bytes,
+                    workspace ? "" : " (NULL)");
+    if (workspace && !aligned(workspace, 256)) return fail(KDA_ERR_MISALIGNED, "workspace is not 256-byte aligned");
+    return KDA_OK;
+}
+
+bool la_sizes_ok(int B, int T, int H, int dk, int dv, int num_seqs, int dtype) {
+    return B >= 1 && T >= 0 && H >= 1 && num_seqs >= 0 && (dk == 64 || dk == 128) && (dv == 64 || dv == 128) &&
+           (dtype == KDA_BF16 || dtype == KDA_F32);
+}
+
+size_t la_forward_ws(int H, int dk, int dv, int num_seqs, bool with_slots) {
+    return kda::la::carry_bytes(kda::la::kSMs, dk, dv) +
+           (with_slots ? (size_t)num_seqs * H * dk * dv * sizeof(float) : 0);
+}
+
+int la_forward(const kda::la::Call &c, const void *q, const void *k, const void *v, const float *s0, void *o,
+               float *last, int dk, int dv, int dtype, void *ws) {
+    cudaError_t e = cudaErrorInvalidValue;
+#define KDA_LA(DK, DV)                                                                                          \
+    if (dk == DK && dv == DV)                                                                                   \
+        e = dtype == KDA_BF16                                                                                   \
+                ? kda::la::simt_forward<DK, DV, __nv_bfloat16>(c, q, k, v, s0, o, last, (float *)ws)            \
+                : kda::la::simt_forward<DK, DV, float>(c, q, k, v, s0, o, last, (float *)ws)
+    KDA_LA(64, 64);
+    KDA_LA(64, 128);
+    KDA_LA(128, 64);
+    KDA_LA(128, 128);
+#undef KDA_LA
+    return e == cudaSuccess ? KDA_OK : cuda_fail(e, "linear attention launch");
+}
+
+int la_step(const void *q, const void *k, const void *v, const float *log_decay, float *state, void *o, int N, int H,
+            int dk, int dv, int dtype, const int32_t *slots, int num_slots, cudaStream_t st) {
+    const unsigned pairs = (unsigned)((long long)N * H);
+#define KDA_LA(DK, DV, TT)                                                                                       \
+    kda::la::la_step_kernel<DK, DV, TT><<<pairs, 256, 0, st>>>((const TT *)q, (const TT *)k, (const TT *)v, log_decay, \
+                                                               state, (TT *)o, slots, num_slots, H)
+#define KDA_LA2(DK, DV)                                                 \
+    if (dk == DK && dv == DV) {                                         \
+        if (dtype == KDA_BF16) KDA_LA(DK, DV, __nv_bfloat16);           \
+        else KDA_LA(DK, DV, float);                                     \
+    }
+    KDA_LA2(64, 64)
+    KDA_LA2(64, 128)
+    KDA_LA2(128, 64)
+    KDA_LA2(128, 128)
+#undef KDA_LA2
+#undef KDA_LA
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? KDA_OK : cuda_fail(e, "la_step launch");
+}
+
+// ------------------------------------------------------------------ group norm
+
+int check_norm(const void *x, const void *y, const float *mean, const float *rstd, const float *weight,
+               const float *bias, const void *gate, long long N, int L, int C, int G, int act, int dtype) {
+    if (N < 0 || L < 1 || C < 1 || G < 1) return fail(KDA_ERR_INVALID_ARG, "bad sizes N=%lld L=%d C=%d G=%d", N, L, C, G);
+    if (C % G) return fail(KDA_ERR_INVALID_ARG, "C=%d is not a multiple of G=%d", C, G);
+    if (act != KDA_ACT_NONE && act != KDA_ACT_SILU && act != KDA_ACT_SIGMOID)
+        return fail(KDA_ERR_INVALID_ARG, "act=%d is not a KDA_ACT_* value", act);
+    if (dtype != KDA_BF16 && dtype != KDA_F32) return fail(KDA_ERR_UNSUPPORTED, "dtype=%d", dtype);
+    if (C > (1 << 24) || L > (1 << 30)) return fail(KDA_ERR_UNSUPPORTED, "C=%d above 2^24 or L=%d above 2^30", C, L);
+    if (N > (1LL << 31) / G / 2 || N > 1LL << 24)
+        return fail(KDA_ERR_UNSUPPORTED, "N=%lld with G=%d: at most 2^24 samples and 2^30 groups", N, G);
+    if (N == 0) return KDA_OK;
+    if (!x || !y || !mean || !rstd) return fail(KDA_ERR_INVALID_ARG, "x, mean, rstd and the outputs are required");
+    const void *p16[] = {x, y, gate};
+    const char *n16[] = {"x", "y (dx)", "gate"};
+    for (int i = 0; i < 3; ++i)
+        if (p16[i] && !aligned(p16[i], 16)) return fail(KDA_ERR_MISALIGNED, "%s is not 16-byte aligned", n16[i]);
+    const void *p4[] = {mean, rstd, weight, bias};
+    for (int i = 0; i < 4; ++i)
+        if (p4[i] && !aligned(p4[i], 4)) return fail(KDA_ERR_MISALIGNED, "an fp32 array is not 4-byte aligned");
+    return KDA_OK;
+}
+
 }  // namespace
 
 namespace kda {
@@ -739,6 +836,163 @@ int kda_gdn_chunk_backward(const void *q, const void *k, const void *v, const fl
     return backward_impl(q, k, v, log_alpha, beta, init_state, d_o, dfinal_state, dq, dk_out, dv_out, dlog_alpha,
                          dbeta, dinit_state, cu_seqlens, B, T, H, dk, dv, num_seqs, dtype, chunk, workspace, ws_bytes,
                          stream, true);
+}
+
+size_t kda_la_chunk_forward_workspace_size(int B, int T, int H, int dk, int dv, int num_seqs, int dtype,
+                                           int with_slots) {
+    if (!la_sizes_ok(B, T, H, dk, dv, num_seqs, dtype) || T == 0 || num_seqs == 0) return 0;
+    return la_forward_ws(H, dk, dv, num_seqs, with_slots != 0);
+}
+
+int kda_la_chunk_forward(const void *q, const void *k, const void *v, const float *log_decay,
+                         const float *init_state, void *o, float *final_state, const int32_t *cu_seqlens, int B,
+                         int T, int H, int dk, int dv, int num_seqs, int dtype, void *workspace, size_t ws_bytes,
+                         void *stream) {
+    int rc = check_la(q, k, v, log_decay, init_state, o, final_state, cu_seqlens, B, T, H, dk, dv, num_seqs, dtype);
+    if (rc) return rc;
+    rc = check_workspace(workspace, ws_bytes,
+                         kda_la_chunk_forward_workspace_size(B, T, H, dk, dv, num_seqs, dtype, 0));
+    if (rc || num_seqs == 0) return rc;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (T == 0) {
+        char msg[256] = "";
+        rc = kda::tc::state_passthrough(init_state, final_state, num_seqs, H, dk, dv, st, msg, sizeof(msg));
+        return rc ? fail(rc, "%s", msg) : KDA_OK;
+    }
+    const kda::la::Call c{cu_seqlens, nullptr, B, T, H, num_seqs, 0, log_decay, st};
+    return la_forward(c, q, k, v, init_state, o, final_state, dk, dv, dtype, workspace);
+}
+
+int kda_la_chunk_forward_slots(const void *q, const void *k, const void *v, const float *log_decay,
+                               float *state_pool, const int32_t *slots, void *o, const int32_t *cu_seqlens, int B,
+                               int T, int H, int dk, int dv, int num_seqs, int num_slots, int dtype,
+                               void *workspace, size_t ws_bytes, void *stream) {
+    int rc = check_la(q, k, v, log_decay, state_pool, o, state_pool, cu_seqlens, B, T, H, dk, dv, num_seqs, dtype);
+    if (rc) return rc;
+    if (num_seqs > 0 && (!state_pool || !slots))
+        return fail(KDA_ERR_INVALID_ARG, "state_pool and slots are required");
+    if (num_slots < 1) return fail(KDA_ERR_INVALID_ARG, "num_slots=%d must be at least 1", num_slots);
+    if (slots && !aligned(slots, 4)) return fail(KDA_ERR_MISALIGNED, "slots is not 4-byte aligned");
+    rc = check_workspace(workspace, ws_bytes,
+                         kda_la_chunk_forward_workspace_size(B, T, H, dk, dv, num_seqs, dtype, 1));
+    if (rc || num_seqs == 0 || T == 0) return rc;   // without tokens the states stay in their slots
+    const kda::la::Call c{cu_seqlens, slots, B, T, H, num_seqs, num_slots, log_decay, (cudaStream_t)stream};
+    return la_forward(c, q, k, v, state_pool, o, state_pool, dk, dv, dtype, workspace);
+}
+
+int kda_la_recurrent_step(const void *q, const void *k, const void *v, const float *log_decay, float *state, void *o,
+                          int N, int H, int dk, int dv, int dtype, void *stream) {
+    int rc = check_decode(q, k, v, log_decay, log_decay, state, o, N, H, dk, dv, dtype, true);
+    if (rc || N == 0) return rc;
+    return la_step(q, k, v, log_decay, state, o, N, H, dk, dv, dtype, nullptr, 0, (cudaStream_t)stream);
+}
+
+int kda_la_recurrent_step_slots(const void *q, const void *k, const void *v, const float *log_decay,
+                                float *state_pool, const int32_t *slots, void *o, int N, int H, int dk, int dv,
+                                int num_slots, int dtype, void *stream) {
+    int rc = check_decode(q, k, v, log_decay, log_decay, state_pool, o, N, H, dk, dv, dtype, true);
+    if (rc || N == 0) return rc;
+    if (!slots) return fail(KDA_ERR_INVALID_ARG, "slots is required");
+    if (!aligned(slots, 4)) return fail(KDA_ERR_MISALIGNED, "slots is not 4-byte aligned");
+    if (num_slots < 1) return fail(KDA_ERR_INVALID_ARG, "num_slots=%d must be at least 1", num_slots);
+    return la_step(q, k, v, log_decay, state_pool, o, N, H, dk, dv, dtype, slots, num_slots, (cudaStream_t)stream);
+}
+
+size_t kda_la_chunk_backward_workspace_size(int B, int T, int H, int dk, int dv, int num_seqs, int dtype) {
+    if (!la_sizes_ok(B, T, H, dk, dv, num_seqs, dtype) || T == 0 || num_seqs == 0) return 0;
+    return 2 * la_forward_ws(H, dk, dv, num_seqs, false);
+}
+
+int kda_la_chunk_backward(const void *q, const void *k, const void *v, const float *log_decay,
+                          const float *init_state, const void *d_o, const float *dfinal_state, void *dq,
+                          void *dk_out, void *dv_out, float *dinit_state, const int32_t *cu_seqlens, int B, int T,
+                          int H, int dk, int dv, int num_seqs, int dtype, void *workspace, size_t ws_bytes,
+                          void *stream) {
+    int rc = check_la(q, k, v, log_decay, init_state, d_o, dfinal_state, cu_seqlens, B, T, H, dk, dv, num_seqs, dtype);
+    if (rc) return rc;
+    if (T > 0 && (!dq || !dk_out || !dv_out)) return fail(KDA_ERR_INVALID_ARG, "dq, dk and dv are required");
+    const void *p16[] = {dq, dk_out, dv_out, dinit_state};
+    const char *n16[] = {"dq", "dk", "dv", "dinit_state"};
+    for (int i = 0; i < 4; ++i)
+        if (p16[i] && !aligned(p16[i], 16)) return fail(KDA_ERR_MISALIGNED, "%s is not 16-byte aligned", n16[i]);
+    rc = check_workspace(workspace, ws_bytes,
+                         kda_la_chunk_backward_workspace_size(B, T, H, dk, dv, num_seqs, dtype));
+    if (rc || num_seqs == 0) return rc;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (T == 0) {
+        char msg[256] = "";
+        rc = kda::tc::state_passthrough(dfinal_state, dinit_state, num_seqs, H, dk, dv, st, msg, sizeof(msg));
+        return rc ? fail(rc, "%s", msg) : KDA_OK;
+    }
+    const kda::la::Call c{cu_seqlens, nullptr, B, T, H, num_seqs, 0, log_decay, st};
+    cudaError_t e = cudaErrorInvalidValue;
+#define KDA_LA(DK, DV)                                                                                             \
+    if (dk == DK && dv == DV)                                                                                      \
+        e = dtype == KDA_BF16                                                                                      \
+                ? kda::la::simt_backward<DK, DV, __nv_bfloat16>(c, q, k, v, d_o, init_state, dfinal_state, dq, dk_out, \
+                                                                dv_out, dinit_state, (float *)workspace)           \
+                : kda::la::simt_backward<DK, DV, float>(c, q, k, v, d_o, init_state, dfinal_state, dq, dk_out, dv_out, \
+                                                        dinit_state, (float *)workspace)
+    KDA_LA(64, 64);
+    KDA_LA(64, 128);
+    KDA_LA(128, 64);
+    KDA_LA(128, 128);
+#undef KDA_LA
+    return e == cudaSuccess ? KDA_OK : cuda_fail(e, "linear attention backward launch");
+}
+
+size_t kda_group_norm_workspace_size(long long N, int L, int C, int G, int dtype, int backward) {
+    if (N < 1 || L < 1 || C < 1 || G < 1 || C % G || (dtype != KDA_BF16 && dtype != KDA_F32)) return 0;
+    return kda::norm::plan_of(N, L, C, G, dtype == KDA_BF16 ? 2 : 4, backward != 0).ws;
+}
+
+int kda_group_norm_forward(const void *x, const float *weight, const float *bias, const void *gate, void *y,
+                           float *mean, float *rstd, long long N, int L, int C, int G, float eps, int act, int dtype,
+                           void *workspace, size_t ws_bytes, void *stream) {
+    int rc = check_norm(x, y, mean, rstd, weight, bias, gate, N, L, C, G, act, dtype);
+    if (rc) return rc;
+    if (!(eps > 0.f)) return fail(KDA_ERR_INVALID_ARG, "eps=%g must be above 0", (double)eps);
+    if (N == 0) return KDA_OK;
+    const int es = dtype == KDA_BF16 ? 2 : 4;
+    const kda::norm::Plan s = kda::norm::plan_of(N, L, C, G, es, false);
+    if ((rc = check_workspace(workspace, ws_bytes, s.ws))) return rc;
+    kda::norm::Args a{};
+    a.x = x; a.gate = gate; a.weight = weight; a.bias = bias; a.y = y; a.mean = mean; a.rstd = rstd; a.eps = eps;
+    a.ws = workspace;
+    const cudaError_t e = es == 2 ? kda::norm::launch<__nv_bfloat16>(s, a, act, false, (cudaStream_t)stream)
+                                  : kda::norm::launch<float>(s, a, act, false, (cudaStream_t)stream);
+    return e == cudaSuccess ? KDA_OK : cuda_fail(e, "group norm launch");
+}
+
+int kda_group_norm_backward(const void *dy, const void *x, const float *mean, const float *rstd, const float *weight,
+                            const float *bias, const void *gate, void *dx, void *dgate, float *dweight, float *dbias,
+                            long long N, int L, int C, int G, int act, int dtype, void *workspace, size_t ws_bytes,
+                            void *stream) {
+    int rc = check_norm(x, dx, mean, rstd, weight, bias, gate, N, L, C, G, act, dtype);
+    if (rc) return rc;
+    if (N == 0) {   // no samples: the sums are empty
+        const size_t bytes = (size_t)C * sizeof(float);
+        cudaError_t e = cudaSuccess;
+        if (dweight) e = cudaMemsetAsync(dweight, 0, bytes, (cudaStream_t)stream);
+        if (dbias && e == cudaSuccess) e = cudaMemsetAsync(dbias, 0, bytes, (cudaStream_t)stream);
+        return e == cudaSuccess ? KDA_OK : cuda_fail(e, "clearing dweight and dbias");
+    }
+    if (!dy) return fail(KDA_ERR_INVALID_ARG, "dy is required");
+    if (gate && !dgate) return fail(KDA_ERR_INVALID_ARG, "dgate is required with a gate");
+    if (!aligned(dy, 16) || (dgate && !aligned(dgate, 16)))
+        return fail(KDA_ERR_MISALIGNED, "dy or dgate is not 16-byte aligned");
+    if ((dweight && !aligned(dweight, 4)) || (dbias && !aligned(dbias, 4)))
+        return fail(KDA_ERR_MISALIGNED, "dweight or dbias is not 4-byte aligned");
+    const int es = dtype == KDA_BF16 ? 2 : 4;
+    const kda::norm::Plan s = kda::norm::plan_of(N, L, C, G, es, true);
+    if ((rc = check_workspace(workspace, ws_bytes, s.ws))) return rc;
+    kda::norm::Args a{};
+    a.dy = dy; a.x = x; a.gate = gate; a.weight = weight; a.bias = bias; a.y = dx; a.dgate = dgate;
+    a.mean = const_cast<float *>(mean); a.rstd = const_cast<float *>(rstd); a.dweight = dweight; a.dbias = dbias;
+    a.ws = workspace;
+    const cudaError_t e = es == 2 ? kda::norm::launch<__nv_bfloat16>(s, a, act, true, (cudaStream_t)stream)
+                                  : kda::norm::launch<float>(s, a, act, true, (cudaStream_t)stream);
+    return e == cudaSuccess ? KDA_OK : cuda_fail(e, "group norm backward launch");
 }
 
 int kda_debug_wait_timeout(long long limit_cycles, void *stream) {

@@ -1,0 +1,840 @@
+// Group norm with an activation, channels last: x [N, L, C], G groups of D = C / G
+// channels; statistics of each (sample, group) over its L positions and D channels.
+//   xhat = (x - mean) rstd,  z = xhat w + b,  y = act(z), or z act(gate) with a gate
+// Backward, for dy:
+//   dz = dy act'(z)  (with a gate: dy act(gate), and dgate = dy z act'(gate))
+//   dw = sum dz xhat,  db = sum dz  over samples and positions
+//   t = dz w,  dx = rstd (t - m1 - xhat m2),  m1, m2 = means of t and t xhat over the group
+// All arithmetic is in fp32; y, dx and dgate are rounded once, at the store.
+//
+// Two forms.  Rows (L = 1, D in whole 16-byte vectors): a group is D contiguous elements
+// held in the registers of part of a warp, one read and one write of every element.
+// Positions (any L, C, D): sums of row tiles, then a second kernel that joins them per group
+// and reads x again (from L2 where it fits).
+#pragma once
+
+#include <algorithm>
+
+#include "kda_common.cuh"
+
+namespace kda {
+namespace norm {
+
+// ------------------------------------------------------------------ element access
+
+template <typename T, int VEC>
+struct Vec;   // VEC consecutive elements, loaded and stored as one access
+template <>
+struct Vec<__nv_bfloat16, 8> {
+    using Raw = uint4;
+    static __device__ __forceinline__ void open(const uint4 &r, float (&f)[8]) {
+        const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(u[i] << 16);
+            f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ uint4 close(const float (&f)[8]) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        return make_uint4(u[0], u[1], u[2], u[3]);
+    }
+};
+template <>
+struct Vec<float, 4> {
+    using Raw = float4;
+    static __device__ __forceinline__ void open(const float4 &r, float (&f)[4]) {
+        f[0] = r.x; f[1] = r.y; f[2] = r.z; f[3] = r.w;
+    }
+    static __device__ __forceinline__ float4 close(const float (&f)[4]) { return make_float4(f[0], f[1], f[2], f[3]); }
+};
+template <>
+struct Vec<__nv_bfloat16, 1> {
+    using Raw = __nv_bfloat16;
+    static __device__ __forceinline__ void open(const Raw &r, float (&f)[1]) { f[0] = __bfloat162float(r); }
+    static __device__ __forceinline__ Raw close(const float (&f)[1]) { return __float2bfloat16_rn(f[0]); }
+};
+template <>
+struct Vec<float, 1> {
+    using Raw = float;
+    static __device__ __forceinline__ void open(const Raw &r, float (&f)[1]) { f[0] = r; }
+    static __device__ __forceinline__ Raw close(const float (&f)[1]) { return f[0]; }
+};
+template <typename T>
+constexpr int vec_of() { return 16 / (int)sizeof(T); }
+
+template <typename T, int VEC>
+__device__ __forceinline__ void load_vec(const T *p, float (&f)[VEC]) {
+    Vec<T, VEC>::open(*reinterpret_cast<const typename Vec<T, VEC>::Raw *>(p), f);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_vec(T *p, const float (&f)[VEC]) {
+    *reinterpret_cast<typename Vec<T, VEC>::Raw *>(p) = Vec<T, VEC>::close(f);
+}
+
+// ------------------------------------------------------------------ activations
+
+// 1 / (1 + e^-x).  The hardware exponential's error (about |x| 2^-23 relative) is far
+// inside a bf16 step; fp32 tensors take the full-precision one.
+template <typename T>
+__device__ __forceinline__ float logistic(float x) {
+    const float e = sizeof(T) == 2 ? __expf(-x) : expf(-x);
+    return __fdividef(1.f, 1.f + e);   // e = inf gives 0
+}
+template <typename T, int ACT>
+__device__ __forceinline__ float act(float x) {
+    return ACT == KDA_ACT_NONE ? x : ACT == KDA_ACT_SILU ? x * logistic<T>(x) : logistic<T>(x);
+}
+// value and slope
+template <typename T, int ACT>
+__device__ __forceinline__ float2 act2(float x) {
+    if (ACT == KDA_ACT_NONE) return make_float2(x, 1.f);
+    const float p = logistic<T>(x);
+    return ACT == KDA_ACT_SILU ? make_float2(x * p, p * fmaf(x, 1.f - p, 1.f)) : make_float2(p, p * (1.f - p));
+}
+
+// one element: z and dy (and the gate's value) -> dz (and dgate)
+template <typename T, int ACT, bool GATE>
+__device__ __forceinline__ float back_act(float z, float dy, float gate, float &dgate) {
+    if (GATE) {
+        const float2 a = act2<T, ACT>(gate);
+        dgate = dy * z * a.y;
+        return dy * a.x;
+    }
+    return dy * act2<T, ACT>(z).y;
+}
+
+// sum over the `lanes` (a power of two) neighbouring lanes of a warp
+__device__ __forceinline__ float lane_sum(float x, int lanes) {
+    for (int o = lanes >> 1; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// ------------------------------------------------------------------ rows form
+
+constexpr int kThreads = 256;
+
+struct RowsGeo {
+    long long rows;   // N G
+    int G, D;
+    int lanes;        // lanes of a row: a power of two, D <= lanes NV VEC
+    int step;         // rows between two rows of one lane group: a multiple of G
+};
+
+// NV vectors of a row in a lane, U rows at a time.  A lane group keeps one group index g,
+// so its weights stay in registers.
+template <typename T, int NV, int U, int ACT, bool GATE>
+__global__ void __launch_bounds__(kThreads) rows_forward_kernel(RowsGeo r, const T *__restrict__ x,
+                                                                const float *__restrict__ weight,
+                                                                const float *__restrict__ bias,
+                                                                const T *__restrict__ gate, T *__restrict__ y,
+                                                                float *__restrict__ mean, float *__restrict__ rstd,
+                                                                float eps) {
+    constexpr int VEC = vec_of<T>();
+    using V = Vec<T, VEC>;
+    const int per = kThreads / r.lanes;
+    const int sl = threadIdx.x & (r.lanes - 1);
+    const long long sub = (long long)blockIdx.x * per + threadIdx.x / r.lanes;
+    const int g = (int)(sub % r.G);
+    const float inv = 1.f / r.D;
+    float wt[NV][VEC], bs[NV][VEC];
+    bool on[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int d = (sl + j * r.lanes) * VEC;
+        on[j] = d < r.D;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            wt[j][e] = on[j] && weight ? weight[(long long)g * r.D + d + e] : 1.f;
+            bs[j][e] = on[j] && bias ? bias[(long long)g * r.D + d + e] : 0.f;
+        }
+    }
+    // whole lane groups leave the loop together with their warp's others (the bound is the warp's first row)
+    const long long warp_first = (long long)blockIdx.x * per + (threadIdx.x & ~31) / r.lanes;
+    for (long long base = 0; warp_first + base < r.rows; base += (long long)r.step * U) {
+        typename V::Raw xr[U][NV], gr[U][NV];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long row = sub + base + (long long)u * r.step;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const long long at = row * r.D + (sl + j * r.lanes) * VEC;
+                if (row < r.rows && on[j]) {
+                    xr[u][j] = *reinterpret_cast<const typename V::Raw *>(x + at);
+                    if (GATE) gr[u][j] = *reinterpret_cast<const typename V::Raw *>(gate + at);
+                } else {
+                    xr[u][j] = typename V::Raw();
+                    if (GATE) gr[u][j] = typename V::Raw();
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long row = sub + base + (long long)u * r.step;
+            float f[NV][VEC];
+            float s = 0.f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                V::open(xr[u][j], f[j]);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) s += f[j][e];   // lanes that hold nothing add zeros
+            }
+            const float m = lane_sum(s, r.lanes) * inv;
+            float q = 0.f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    f[j][e] -= m;
+                    if (on[j]) q = fmaf(f[j][e], f[j][e], q);
+                }
+            const float rs = rsqrtf(lane_sum(q, r.lanes) * inv + eps);
+            if (row >= r.rows) continue;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                if (!on[j]) continue;
+                float gv[VEC], out[VEC];
+                if (GATE) V::open(gr[u][j], gv);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float z = fmaf(f[j][e] * rs, wt[j][e], bs[j][e]);
+                    out[e] = GATE ? z * act<T, ACT>(gv[e]) : act<T, ACT>(z);
+                }
+                store_vec<T, VEC>(y + row * r.D + (sl + j * r.lanes) * VEC, out);
+            }
+            if (sl == 0) {
+                mean[row] = m;
+                rstd[row] = rs;
+            }
+        }
+    }
+}
+
+// part: [step / G][2][C] sums of dz xhat and dz over each lane group's rows
+template <typename T, int NV, int ACT, bool GATE>
+__global__ void __launch_bounds__(kThreads) rows_backward_kernel(RowsGeo r, const T *__restrict__ dy,
+                                                                 const T *__restrict__ x,
+                                                                 const float *__restrict__ mean,
+                                                                 const float *__restrict__ rstd,
+                                                                 const float *__restrict__ weight,
+                                                                 const float *__restrict__ bias,
+                                                                 const T *__restrict__ gate, T *__restrict__ dx,
+                                                                 T *__restrict__ dgate, float *__restrict__ part) {
+    constexpr int VEC = vec_of<T>();
+    using V = Vec<T, VEC>;
+    const int per = kThreads / r.lanes;
+    const int sl = threadIdx.x & (r.lanes - 1);
+    const long long sub = (long long)blockIdx.x * per + threadIdx.x / r.lanes;
+    const int g = (int)(sub % r.G);
+    const float inv = 1.f / r.D;
+    float wt[NV][VEC], bs[NV][VEC], dw[NV][VEC] = {}, db[NV][VEC] = {};
+    bool on[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int d = (sl + j * r.lanes) * VEC;
+        on[j] = d < r.D;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            wt[j][e] = on[j] && weight ? weight[(long long)g * r.D + d + e] : 1.f;
+            bs[j][e] = on[j] && bias ? bias[(long long)g * r.D + d + e] : 0.f;
+        }
+    }
+    const long long warp_first = (long long)blockIdx.x * per + (threadIdx.x & ~31) / r.lanes;
+    for (long long base = 0; warp_first + base < r.rows; base += r.step) {
+        const long long row = sub + base;
+        const bool in = row < r.rows;
+        typename V::Raw xr[NV], yr[NV], gr[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const long long at = row * r.D + (sl + j * r.lanes) * VEC;
+            xr[j] = yr[j] = gr[j] = typename V::Raw();
+            if (in && on[j]) {
+                xr[j] = *reinterpret_cast<const typename V::Raw *>(x + at);
+                yr[j] = *reinterpret_cast<const typename V::Raw *>(dy + at);
+                if (GATE) gr[j] = *reinterpret_cast<const typename V::Raw *>(gate + at);
+            }
+        }
+        const float m = in ? mean[row] : 0.f, rs = in ? rstd[row] : 0.f;
+        float xh[NV][VEC], t[NV][VEC];
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float dv[VEC], gv[VEC], dg[VEC];
+            V::open(xr[j], xh[j]);
+            V::open(yr[j], dv);
+            if (GATE) V::open(gr[j], gv);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const float h = (xh[j][e] - m) * rs;
+                const float z = fmaf(h, wt[j][e], bs[j][e]);
+                // where there is no element dy is 0, and so is dz
+                const float dz = back_act<T, ACT, GATE>(z, dv[e], GATE ? gv[e] : 0.f, dg[e]);
+                xh[j][e] = h;
+                t[j][e] = dz * wt[j][e];
+                dw[j][e] = fmaf(dz, h, dw[j][e]);
+                db[j][e] += dz;
+                s1 += t[j][e];
+                s2 = fmaf(t[j][e], h, s2);
+            }
+            if (GATE && in && on[j]) store_vec<T, VEC>(dgate + row * r.D + (sl + j * r.lanes) * VEC, dg);
+        }
+        s1 = lane_sum(s1, r.lanes) * inv;
+        s2 = lane_sum(s2, r.lanes) * inv;
+        if (!in) continue;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if (!on[j]) continue;
+            float out[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) out[e] = rs * (t[j][e] - s1 - xh[j][e] * s2);
+            store_vec<T, VEC>(dx + row * r.D + (sl + j * r.lanes) * VEC, out);
+        }
+    }
+    const long long C = (long long)r.G * r.D;
+    float *p = part + (sub / r.G) * 2 * C + (long long)g * r.D;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        if (on[j])
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                p[(sl + j * r.lanes) * VEC + e] = dw[j][e];
+                p[C + (sl + j * r.lanes) * VEC + e] = db[j][e];
+            }
+}
+
+// ------------------------------------------------------------------ positions form
+
+// A CTA takes one row tile of one sample and one block of at most 256 vectors of channels:
+// blockIdx.x = n tiles + tile, blockIdx.y = channel block.
+struct PosGeo {
+    int N, L, C, G, D;
+    int tiles, tile_rows;   // row tiles of a sample
+    int cvecs;              // C / VEC
+    int tpr;                // threads of one row: min(cvecs, 256); a CTA holds 256 / tpr rows at a time
+    int Z;                  // channel blocks: ceil(cvecs / tpr)
+    __device__ __forceinline__ int rows_of(int tile) const { return min(tile_rows, L - tile * tile_rows); }
+};
+
+// The channels of block z, and of them those of group g.
+template <int VEC>
+struct Block {
+    int c0, c1, g0, g1;
+    __device__ __forceinline__ Block(const PosGeo &p, int z) {
+        c0 = z * p.tpr * VEC;
+        c1 = min(p.C, c0 + p.tpr * VEC);
+        g0 = c0 / p.D;
+        g1 = (c1 - 1) / p.D;
+    }
+};
+template <int VEC>
+__device__ __forceinline__ int channels_in(const PosGeo &p, int z, int g) {
+    const Block<VEC> b(p, z);
+    return min(b.c1, (g + 1) * p.D) - max(b.c0, g * p.D);
+}
+// Partial of (n, g, tile, z)
+__device__ __forceinline__ long long part_at(const PosGeo &p, int n, int g, int tile, int z) {
+    return (((long long)n * p.G + g) * p.tiles + tile) * p.Z + z;
+}
+
+// Chan's update: (n, mean, m2) joined with (nb, meanb, m2b)
+__device__ __forceinline__ void join_moments(float &n, float &mean, float &m2, float nb, float meanb, float m2b) {
+    if (nb == 0.f) return;
+    const float t = n + nb, d = meanb - mean, f = nb / t;
+    mean = fmaf(d, f, mean);
+    m2 += fmaf(d * d, n * f, m2b);
+    n = t;
+}
+__device__ __forceinline__ void warp_join_moments(float &n, float &mean, float &m2) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const float nb = __shfl_xor_sync(0xffffffffu, n, o), mb = __shfl_xor_sync(0xffffffffu, mean, o),
+                    qb = __shfl_xor_sync(0xffffffffu, m2, o);
+        join_moments(n, mean, m2, nb, mb, qb);
+    }
+}
+
+// Moments of a row tile and channel block for each group it touches: part[n][g][tile][z] =
+// (mean, m2).  A thread takes eight rows of its channels at a time: their mean, then their
+// centred squares, joined to what it has, so that no large mean cancels in a difference of sums.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kThreads) pos_moments_kernel(PosGeo p, const T *__restrict__ x,
+                                                               float2 *__restrict__ part) {
+    __shared__ float sm_m[VEC * kThreads], sm_q[VEC * kThreads];
+    const int tile = blockIdx.x % p.tiles, n = blockIdx.x / p.tiles, z = blockIdx.y;
+    const int rl = threadIdx.x / p.tpr, cl = threadIdx.x % p.tpr, rows = kThreads / p.tpr;
+    const int r0 = tile * p.tile_rows, r1 = r0 + p.rows_of(tile);
+    const int cv = z * p.tpr + cl;
+    float mean[VEC] = {}, m2[VEC] = {}, cnt = 0.f;
+    if (rl < rows && cv < p.cvecs)
+        for (int r = r0 + rl; r < r1; r += 8 * rows) {
+            float f[8][VEC];
+            int k = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (r + i * rows < r1) {
+                    load_vec<T, VEC>(x + ((long long)n * p.L + r + i * rows) * p.C + (long long)cv * VEC, f[i]);
+                    k = i + 1;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) f[i][e] = 0.f;
+                }
+            const float nb = (float)k, ik = 1.f / nb, t = cnt + nb, fr = nb / t;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                float s = 0.f, q = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s += f[i][e];
+                const float mb = s * ik;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < k) q = fmaf(f[i][e] - mb, f[i][e] - mb, q);
+                const float d = mb - mean[e];
+                mean[e] = fmaf(d, fr, mean[e]);
+                m2[e] += fmaf(d * d, cnt * fr, q);
+            }
+            cnt = t;
+        }
+    // entry (row lane, channel of the block): [row lane][tpr VEC]
+    if (rl < rows)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            sm_m[(rl * p.tpr + cl) * VEC + e] = mean[e];
+            sm_q[(rl * p.tpr + cl) * VEC + e] = m2[e];
+        }
+    __syncthreads();
+    const Block<VEC> b(p, z);
+    const int lane = threadIdx.x & 31;
+    for (int g = b.g0 + (int)threadIdx.x / 32; g <= b.g1; g += kThreads / 32) {
+        const int first = max(b.c0, g * p.D) - b.c0, w = channels_in<VEC>(p, z, g);
+        float c = 0.f, m = 0.f, q = 0.f;
+        for (int i = lane; i < rows * w; i += 32) {
+            const int ri = i / w, at = ri * p.tpr * VEC + first + (i - ri * w);
+            // rows of lane ri: r0 + ri, then every `rows`
+            const int have = max(0, (r1 - r0 - ri + rows - 1) / rows);
+            join_moments(c, m, q, (float)have, sm_m[at], sm_q[at]);
+        }
+        warp_join_moments(c, m, q);
+        if (lane == 0) part[part_at(p, n, g, tile, z)] = make_float2(m, q);
+    }
+}
+
+// y from x and the partial moments.  Each CTA joins the moments of its groups (the CTAs of
+// tile 0 store them), then runs down its rows.
+template <typename T, int VEC, int ACT, bool GATE>
+__global__ void __launch_bounds__(kThreads) pos_apply_kernel(PosGeo p, const T *__restrict__ x,
+                                                             const float *__restrict__ weight,
+                                                             const float *__restrict__ bias,
+                                                             const T *__restrict__ gate, T *__restrict__ y,
+                                                             const float2 *__restrict__ part,
+                                                             float *__restrict__ mean, float *__restrict__ rstd,
+                                                             float eps) {
+    __shared__ float2 stat[VEC * kThreads];   // (mean, rstd) of the block's groups
+    const int tile = blockIdx.x % p.tiles, n = blockIdx.x / p.tiles, z = blockIdx.y;
+    const Block<VEC> b(p, z);
+    const int lane = threadIdx.x & 31;
+    for (int g = b.g0 + (int)threadIdx.x / 32; g <= b.g1; g += kThreads / 32) {
+        const int z0 = g * p.D / (p.tpr * VEC), zn = ((g + 1) * p.D - 1) / (p.tpr * VEC) - z0 + 1;
+        float c = 0.f, m = 0.f, q = 0.f;
+        for (int i = lane; i < p.tiles * zn; i += 32) {
+            const int t = i / zn, zz = z0 + i - t * zn;
+            const float2 v = part[part_at(p, n, g, t, zz)];
+            join_moments(c, m, q, (float)p.rows_of(t) * channels_in<VEC>(p, zz, g), v.x, v.y);
+        }
+        warp_join_moments(c, m, q);
+        const float rs = rsqrtf(q / c + eps);
+        if (lane == 0) {
+            stat[g - b.g0] = make_float2(m, rs);
+            if (tile == 0 && z == z0) {
+                mean[(long long)n * p.G + g] = m;
+                rstd[(long long)n * p.G + g] = rs;
+            }
+        }
+    }
+    __syncthreads();
+    const int rl = threadIdx.x / p.tpr, cl = threadIdx.x % p.tpr, rows = kThreads / p.tpr;
+    const int r0 = tile * p.tile_rows, r1 = r0 + p.rows_of(tile);
+    const int cv = z * p.tpr + cl;
+    if (rl >= rows || cv >= p.cvecs) return;
+    float m[VEC], s[VEC], o[VEC];   // z = (x - m) s + o
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        const int c = cv * VEC + e;
+        const float2 v = stat[c / p.D - b.g0];
+        m[e] = v.x;
+        s[e] = v.y * (weight ? weight[c] : 1.f);
+        o[e] = bias ? bias[c] : 0.f;
+    }
+    for (int r = r0 + rl; r < r1; r += 4 * rows) {
+        float f[4][VEC], gv[4][VEC];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (r + i * rows < r1) {
+                const long long at = ((long long)n * p.L + r + i * rows) * p.C + (long long)cv * VEC;
+                load_vec<T, VEC>(x + at, f[i]);
+                if (GATE) load_vec<T, VEC>(gate + at, gv[i]);
+            }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (r + i * rows < r1) {
+                float out[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float zz = fmaf(f[i][e] - m[e], s[e], o[e]);
+                    out[e] = GATE ? zz * act<T, ACT>(gv[i][e]) : act<T, ACT>(zz);
+                }
+                store_vec<T, VEC>(y + ((long long)n * p.L + r + i * rows) * p.C + (long long)cv * VEC, out);
+            }
+    }
+}
+
+// Per-channel values of one thread of the backward kernels
+template <int VEC>
+struct Affine {
+    float m[VEC], rs[VEC], wt[VEC], bs[VEC];
+    __device__ __forceinline__ Affine(const PosGeo &p, int n, int cv, const float *mean, const float *rstd,
+                                      const float *weight, const float *bias) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const int c = cv * VEC + e;
+            const long long i = (long long)n * p.G + c / p.D;
+            m[e] = mean[i];
+            rs[e] = rstd[i];
+            wt[e] = weight ? weight[c] : 1.f;
+            bs[e] = bias ? bias[c] : 0.f;
+        }
+    }
+};
+
+// Backward: sums of a row tile.  Per channel chan[n][tile][c] = (sum dz xhat, sum dz); per
+// group part[n][g][tile][z] = (sum w dz, sum w dz xhat).  dgate is written here.
+template <typename T, int VEC, int ACT, bool GATE>
+__global__ void __launch_bounds__(kThreads) pos_back_sums_kernel(
+    PosGeo p, const T *__restrict__ dy, const T *__restrict__ x, const float *__restrict__ mean,
+    const float *__restrict__ rstd, const float *__restrict__ weight, const float *__restrict__ bias,
+    const T *__restrict__ gate, T *__restrict__ dgate, float2 *__restrict__ chan, float2 *__restrict__ part) {
+    __shared__ float sm_w[VEC * kThreads], sm_b[VEC * kThreads];
+    const int tile = blockIdx.x % p.tiles, n = blockIdx.x / p.tiles, z = blockIdx.y;
+    const int rl = threadIdx.x / p.tpr, cl = threadIdx.x % p.tpr, rows = kThreads / p.tpr;
+    const int r0 = tile * p.tile_rows, r1 = r0 + p.rows_of(tile);
+    const int cv = z * p.tpr + cl;
+    const bool on = rl < rows && cv < p.cvecs;
+    float dw[VEC] = {}, db[VEC] = {};
+    if (on) {
+        const Affine<VEC> a(p, n, cv, mean, rstd, weight, bias);
+        for (int r = r0 + rl; r < r1; r += 2 * rows) {
+            float f[2][VEC], dv[2][VEC], gv[2][VEC];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (r + i * rows < r1) {
+                    const long long at = ((long long)n * p.L + r + i * rows) * p.C + (long long)cv * VEC;
+                    load_vec<T, VEC>(x + at, f[i]);
+                    load_vec<T, VEC>(dy + at, dv[i]);
+                    if (GATE) load_vec<T, VEC>(gate + at, gv[i]);
+                }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (r + i * rows < r1) {
+                    float dg[VEC];
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const float h = (f[i][e] - a.m[e]) * a.rs[e];
+                        const float zz = fmaf(h, a.wt[e], a.bs[e]);
+                        const float dz = back_act<T, ACT, GATE>(zz, dv[i][e], GATE ? gv[i][e] : 0.f, dg[e]);
+                        dw[e] = fmaf(dz, h, dw[e]);
+                        db[e] += dz;
+                    }
+                    if (GATE)
+                        store_vec<T, VEC>(dgate + ((long long)n * p.L + r + i * rows) * p.C + (long long)cv * VEC, dg);
+                }
+        }
+    }
+    if (rl < rows)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            sm_w[(rl * p.tpr + cl) * VEC + e] = dw[e];
+            sm_b[(rl * p.tpr + cl) * VEC + e] = db[e];
+        }
+    __syncthreads();
+    // the row lanes of each channel, in order; the sums stay in row lane 0's entries
+    const Block<VEC> b(p, z);
+    const int span = p.tpr * VEC;
+    for (int i = threadIdx.x; i < b.c1 - b.c0; i += kThreads) {
+        float2 v = make_float2(sm_w[i], sm_b[i]);
+        for (int k = 1; k < rows; ++k) {
+            v.x += sm_w[k * span + i];
+            v.y += sm_b[k * span + i];
+        }
+        chan[((long long)n * p.tiles + tile) * p.C + b.c0 + i] = v;
+        sm_w[i] = v.x;
+        sm_b[i] = v.y;
+    }
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    for (int g = b.g0 + (int)threadIdx.x / 32; g <= b.g1; g += kThreads / 32) {
+        const int first = max(b.c0, g * p.D), w = channels_in<VEC>(p, z, g);
+        float s1 = 0.f, s2 = 0.f;
+        for (int i = lane; i < w; i += 32) {
+            const float wt = weight ? weight[first + i] : 1.f;
+            s1 = fmaf(wt, sm_b[first - b.c0 + i], s1);
+            s2 = fmaf(wt, sm_w[first - b.c0 + i], s2);
+        }
+        s1 = lane_sum(s1, 32);
+        s2 = lane_sum(s2, 32);
+        if (lane == 0) part[part_at(p, n, g, tile, z)] = make_float2(s1, s2);
+    }
+}
+
+// dx; the CTAs behind the N tiles row tiles (blockIdx.y 0) sum dweight and dbias, 32 channels each.
+template <typename T, int VEC, int ACT, bool GATE>
+__global__ void __launch_bounds__(kThreads) pos_back_apply_kernel(
+    PosGeo p, const T *__restrict__ dy, const T *__restrict__ x, const float *__restrict__ mean,
+    const float *__restrict__ rstd, const float *__restrict__ weight, const float *__restrict__ bias,
+    const T *__restrict__ gate, T *__restrict__ dx, const float2 *__restrict__ chan, const float2 *__restrict__ part,
+    float *__restrict__ dweight, float *__restrict__ dbias) {
+    __shared__ float2 stat[VEC * kThreads];   // (m1, m2) of the block's groups
+    const int lane = threadIdx.x & 31;
+    if ((int)blockIdx.x >= p.N * p.tiles) {
+        if (blockIdx.y) return;
+        const int wp = threadIdx.x / 32, c = ((int)blockIdx.x - p.N * p.tiles) * 32 + lane;
+        float2 v = make_float2(0.f, 0.f);
+        if (c < p.C)
+            for (int k = wp; k < p.N * p.tiles; k += kThreads / 32) {
+                const float2 u = chan[(long long)k * p.C + c];
+                v.x += u.x;
+                v.y += u.y;
+            }
+        stat[threadIdx.x] = v;
+        __syncthreads();
+        if (wp == 0 && c < p.C) {
+#pragma unroll
+            for (int i = 1; i < kThreads / 32; ++i) {
+                v.x += stat[i * 32 + lane].x;
+                v.y += stat[i * 32 + lane].y;
+            }
+            if (dweight) dweight[c] = v.x;
+            if (dbias) dbias[c] = v.y;
+        }
+        return;
+    }
+    const int tile = blockIdx.x % p.tiles, n = blockIdx.x / p.tiles, z = blockIdx.y;
+    const Block<VEC> b(p, z);
+    const float inv = 1.f / ((float)p.L * p.D);
+    for (int g = b.g0 + (int)threadIdx.x / 32; g <= b.g1; g += kThreads / 32) {
+        const int z0 = g * p.D / (p.tpr * VEC), zn = ((g + 1) * p.D - 1) / (p.tpr * VEC) - z0 + 1;
+        float s1 = 0.f, s2 = 0.f;
+        for (int i = lane; i < p.tiles * zn; i += 32) {
+            const int t = i / zn;
+            const float2 v = part[part_at(p, n, g, t, z0 + i - t * zn)];
+            s1 += v.x;
+            s2 += v.y;
+        }
+        s1 = lane_sum(s1, 32);
+        s2 = lane_sum(s2, 32);
+        if (lane == 0) stat[g - b.g0] = make_float2(s1 * inv, s2 * inv);
+    }
+    __syncthreads();
+    const int rl = threadIdx.x / p.tpr, cl = threadIdx.x % p.tpr, rows = kThreads / p.tpr;
+    const int r0 = tile * p.tile_rows, r1 = r0 + p.rows_of(tile);
+    const int cv = z * p.tpr + cl;
+    if (rl >= rows || cv >= p.cvecs) return;
+    const Affine<VEC> a(p, n, cv, mean, rstd, weight, bias);
+    float2 mm[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) mm[e] = stat[(cv * VEC + e) / p.D - b.g0];
+    for (int r = r0 + rl; r < r1; r += 2 * rows) {
+        float f[2][VEC], dv[2][VEC], gv[2][VEC];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (r + i * rows < r1) {
+                const long long at = ((long long)n * p.L + r + i * rows) * p.C + (long long)cv * VEC;
+                load_vec<T, VEC>(x + at, f[i]);
+                load_vec<T, VEC>(dy + at, dv[i]);
+                if (GATE) load_vec<T, VEC>(gate + at, gv[i]);
+            }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (r + i * rows < r1) {
+                float out[VEC], dg;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float h = (f[i][e] - a.m[e]) * a.rs[e];
+                    const float zz = fmaf(h, a.wt[e], a.bs[e]);
+                    const float dz = back_act<T, ACT, GATE>(zz, dv[i][e], GATE ? gv[i][e] : 0.f, dg);
+                    out[e] = a.rs[e] * (dz * a.wt[e] - mm[e].x - h * mm[e].y);
+                }
+                store_vec<T, VEC>(dx + ((long long)n * p.L + r + i * rows) * p.C + (long long)cv * VEC, out);
+            }
+    }
+}
+
+// dweight, dbias from the rows form's partial sums [reps][2][C]: 32 channels a CTA.
+__global__ void __launch_bounds__(kThreads) rows_back_join_kernel(const float *__restrict__ part, int reps,
+                                                                  long long C, float *__restrict__ dweight,
+                                                                  float *__restrict__ dbias) {
+    __shared__ float2 s[kThreads / 32][32];
+    const int lane = threadIdx.x & 31, wp = threadIdx.x / 32;
+    const long long c = (long long)blockIdx.x * 32 + lane;
+    float2 v = make_float2(0.f, 0.f);
+    if (c < C)
+        for (int k = wp; k < reps; k += kThreads / 32) {
+            v.x += part[k * 2 * C + c];
+            v.y += part[(k * 2 + 1) * C + c];
+        }
+    s[wp][lane] = v;
+    __syncthreads();
+    if (wp == 0 && c < C) {
+#pragma unroll
+        for (int i = 1; i < kThreads / 32; ++i) {
+            v.x += s[i][lane].x;
+            v.y += s[i][lane].y;
+        }
+        if (dweight) dweight[c] = v.x;
+        if (dbias) dbias[c] = v.y;
+    }
+}
+
+}  // namespace norm
+}  // namespace kda
+
+// ------------------------------------------------------------------ host side
+
+namespace kda {
+namespace norm {
+
+constexpr int kSMs = 148;
+
+struct Plan {
+    bool rows;          // rows form
+    RowsGeo r;
+    int nv, row_blocks;
+    PosGeo p;
+    bool vec;           // positions form: 16-byte vectors
+    size_t ws;          // workspace bytes
+};
+
+inline long long gcd_of(long long a, long long b) { return b ? gcd_of(b, a % b) : a; }
+
+// Rows form up to four vectors a lane (D <= 1024 bf16, 512 fp32); beyond that, or with
+// several positions, the statistics span CTAs.
+inline Plan plan_of(long long N, int L, int C, int G, int esize, bool backward) {
+    Plan s{};
+    const int vw = 16 / esize, D = C / G;
+    if (L == 1 && D % vw == 0 && D / vw <= 128) {
+        s.rows = true;
+        const int vecs = D / vw;
+        int lanes = 1;
+        while (lanes < vecs && lanes < 32) lanes *= 2;
+        const int nv = (vecs + lanes - 1) / lanes;
+        s.nv = nv <= 2 ? nv : 4;
+        const long long rows = N * G, per = kThreads / lanes;
+        const long long unit = G / gcd_of(G, per);   // blocks whose lane groups are a multiple of G
+        const long long want = std::min<long long>((rows + per - 1) / per, (long long)kSMs * 8);
+        s.row_blocks = (int)((want + unit - 1) / unit * unit);
+        s.r = RowsGeo{rows, G, D, lanes, (int)(s.row_blocks * per)};
+        s.ws = backward ? (size_t)(s.r.step / G) * 2 * C * sizeof(float) : 0;
+        return s;
+    }
+    s.vec = C % vw == 0;
+    PosGeo &p = s.p;
+    p.N = (int)N; p.L = L; p.C = C; p.G = G; p.D = D;
+    p.cvecs = s.vec ? C / vw : C;
+    p.tpr = std::min(p.cvecs, kThreads);
+    p.Z = (p.cvecs + p.tpr - 1) / p.tpr;
+    const int rows = kThreads / p.tpr;                       // rows a CTA holds at a time
+    const long long want = std::max<long long>(1, 2 * kSMs / (N * p.Z));   // tiles of a sample: two CTAs per SM
+    const long long tr = std::max<long long>((L + want - 1) / want, (long long)8 * rows);
+    p.tile_rows = (int)std::min<long long>(tr, L);
+    p.tiles = (L + p.tile_rows - 1) / p.tile_rows;
+    const size_t group = (size_t)N * G * p.tiles * p.Z * sizeof(float2);
+    s.ws = group + (backward ? (size_t)N * p.tiles * C * sizeof(float2) : 0);
+    return s;
+}
+
+struct Args {
+    const void *dy, *x, *gate;
+    const float *weight, *bias;
+    void *y, *dgate;          // y or dx
+    float *mean, *rstd;       // backward: read only
+    float *dweight, *dbias;
+    float eps;
+    void *ws;
+};
+
+template <typename T, int ACT, bool GATE>
+cudaError_t launch_forward(const Plan &s, const Args &a, cudaStream_t st) {
+    constexpr int VW = vec_of<T>();
+    const T *x = (const T *)a.x, *gate = (const T *)a.gate;
+    T *y = (T *)a.y;
+    if (s.rows) {
+#define KDA_ROWS(NV, U)                                                                                         \
+    rows_forward_kernel<T, NV, U, ACT, GATE><<<s.row_blocks, kThreads, 0, st>>>(s.r, x, a.weight, a.bias, gate, y, \
+                                                                                a.mean, a.rstd, a.eps)
+        if (s.nv == 1) KDA_ROWS(1, 4);
+        else if (s.nv == 2) KDA_ROWS(2, 2);
+        else KDA_ROWS(4, 1);
+#undef KDA_ROWS
+        return cudaGetLastError();
+    }
+    const dim3 grid((unsigned)((long long)s.p.N * s.p.tiles), s.p.Z);
+    float2 *part = (float2 *)a.ws;
+#define KDA_POS(VEC)                                                                                      \
+    pos_moments_kernel<T, VEC><<<grid, kThreads, 0, st>>>(s.p, x, part);                                  \
+    pos_apply_kernel<T, VEC, ACT, GATE><<<grid, kThreads, 0, st>>>(s.p, x, a.weight, a.bias, gate, y, part, \
+                                                                   a.mean, a.rstd, a.eps)
+    if (s.vec) { KDA_POS(VW); } else { KDA_POS(1); }
+#undef KDA_POS
+    return cudaGetLastError();
+}
+
+template <typename T, int ACT, bool GATE>
+cudaError_t launch_backward(const Plan &s, const Args &a, cudaStream_t st) {
+    constexpr int VW = vec_of<T>();
+    const T *dy = (const T *)a.dy, *x = (const T *)a.x, *gate = (const T *)a.gate;
+    T *dx = (T *)a.y, *dgate = (T *)a.dgate;
+    if (s.rows) {
+        float *part = (float *)a.ws;
+        const long long C = (long long)s.r.G * s.r.D;
+#define KDA_ROWS(NV)                                                                                            \
+    rows_backward_kernel<T, NV, ACT, GATE><<<s.row_blocks, kThreads, 0, st>>>(s.r, dy, x, a.mean, a.rstd, a.weight, \
+                                                                              a.bias, gate, dx, dgate, part)
+        if (s.nv == 1) KDA_ROWS(1);
+        else if (s.nv == 2) KDA_ROWS(2);
+        else KDA_ROWS(4);
+#undef KDA_ROWS
+        if (a.dweight || a.dbias)
+            rows_back_join_kernel<<<(unsigned)((C + 31) / 32), kThreads, 0, st>>>(part, s.r.step / s.r.G, C, a.dweight,
+                                                                                  a.dbias);
+        return cudaGetLastError();
+    }
+    const long long tiles = (long long)s.p.N * s.p.tiles;
+    const dim3 grid((unsigned)tiles, s.p.Z);
+    const unsigned join = a.dweight || a.dbias ? (s.p.C + 31) / 32 : 0;
+    float2 *part = (float2 *)a.ws, *chan = part + (size_t)s.p.N * s.p.G * s.p.tiles * s.p.Z;
+#define KDA_POS(VEC)                                                                                              \
+    pos_back_sums_kernel<T, VEC, ACT, GATE><<<grid, kThreads, 0, st>>>(s.p, dy, x, a.mean, a.rstd, a.weight, a.bias, \
+                                                                       gate, dgate, chan, part);                  \
+    pos_back_apply_kernel<T, VEC, ACT, GATE><<<dim3(grid.x + join, grid.y), kThreads, 0, st>>>(                   \
+        s.p, dy, x, a.mean, a.rstd, a.weight, a.bias, gate, dx, chan, part, a.dweight, a.dbias)
+    if (s.vec) { KDA_POS(VW); } else { KDA_POS(1); }
+#undef KDA_POS
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch(const Plan &s, const Args &a, int act, bool backward, cudaStream_t st) {
+#define KDA_NORM(ACT)                                                                                       \
+    return backward ? (a.gate ? launch_backward<T, ACT, true>(s, a, st) : launch_backward<T, ACT, false>(s, a, st)) \
+                    : (a.gate ? launch_forward<T, ACT, true>(s, a, st) : launch_forward<T, ACT, false>(s, a, st))
+    if (act == KDA_ACT_NONE) KDA_NORM(KDA_ACT_NONE);
+    if (act == KDA_ACT_SILU) KDA_NORM(KDA_ACT_SILU);
+    KDA_NORM(KDA_ACT_SIGMOID);
+#undef KDA_NORM
+}
+
+}  // namespace norm
+}  // namespace kda

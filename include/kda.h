@@ -431,6 +431,104 @@ int kda_gdn_chunk_backward_ex(const void *q, const void *k, const void *v, const
                               int dk, int dv, int num_seqs, int dtype, int chunk, void *workspace, size_t ws_bytes,
                               void *stream, int algo);
 
+/*
+ * Linear attention with a decay for each head: the recurrence without the delta
+ * write and with one constant rate per head,
+ *
+ *     S = exp(log_decay_h) S + k_t v_t^T,   o_t = S^T q_t
+ *
+ * the plain linear attention that the pages start from ("Kimi Delta Attention
+ * 徹底解説" (tech-tide.dev), § "なぜ今「線形アテンション」なのか": the running sum of
+ * k v^T) with a fixed forgetting rate for each head.  Layouts, states, packing,
+ * ownership and errors are those of the calls above, so a layer can use either
+ * operator on the same buffers.
+ *
+ *   q, k, v, o    as in kda_chunk_forward
+ *   log_decay     fp32 [H] on the device, <= 0 and finite (0: nothing is forgotten)
+ *   init_state, final_state, cu_seqlens, B, T, H, dk, dv, num_seqs, dtype
+ *                 as in kda_chunk_forward
+ *   workspace     kda_la_chunk_forward_workspace_size() bytes, 256-byte aligned
+ *                 (30 MB at most plus, with slots, one state per sequence and head,
+ *                 whatever T); calls that can overlap in time need their own
+ * KDA_BF16 runs on the tensor cores with fp32 accumulation: o is rounded once more
+ * than bf16 inputs need (the decayed scores and the state that o reads are bf16
+ * operands), while final_state keeps fp32 accuracy.  KDA_F32 runs in fp32.
+ * Rows of o behind the last packed sequence are not written.
+ */
+size_t kda_la_chunk_forward_workspace_size(int B, int T, int H, int dk, int dv, int num_seqs, int dtype,
+                                           int with_slots);
+
+int kda_la_chunk_forward(const void *q, const void *k, const void *v, const float *log_decay,
+                         const float *init_state, void *o, float *final_state, const int32_t *cu_seqlens, int B,
+                         int T, int H, int dk, int dv, int num_seqs, int dtype, void *workspace, size_t ws_bytes,
+                         void *stream);
+
+/* The same from and into a state pool; state_pool, slots and num_slots as in
+ * kda_chunk_forward_slots.  The workspace size is the one with with_slots = 1. */
+int kda_la_chunk_forward_slots(const void *q, const void *k, const void *v, const float *log_decay,
+                               float *state_pool, const int32_t *slots, void *o, const int32_t *cu_seqlens, int B,
+                               int T, int H, int dk, int dv, int num_seqs, int num_slots, int dtype,
+                               void *workspace, size_t ws_bytes, void *stream);
+
+/* One token per sequence, the state updated in place; shapes as in
+ * kda_recurrent_step and kda_recurrent_step_slots, log_decay fp32 [H]. */
+int kda_la_recurrent_step(const void *q, const void *k, const void *v, const float *log_decay, float *state,
+                          void *o, int N, int H, int dk, int dv, int dtype, void *stream);
+
+int kda_la_recurrent_step_slots(const void *q, const void *k, const void *v, const float *log_decay,
+                                float *state_pool, const int32_t *slots, void *o, int N, int H, int dk, int dv,
+                                int num_slots, int dtype, void *stream);
+
+/*
+ * Gradients of sum <d_o, o> + <dfinal_state, final_state> through
+ * kda_la_chunk_forward.  The rates are constants of the model: there is no
+ * gradient for log_decay.
+ *   d_o           [B, T, H, dv] in dtype;  dfinal_state fp32 [N, H, dk, dv] or NULL (zero)
+ *   dq, dk_out    [B, T, H, dk], dv_out [B, T, H, dv] in dtype, overwritten
+ *   dinit_state   fp32 [N, H, dk, dv] or NULL (not computed)
+ *   workspace     kda_la_chunk_backward_workspace_size() bytes, 256-byte aligned
+ * Tokens outside every packed sequence are not written.
+ */
+size_t kda_la_chunk_backward_workspace_size(int B, int T, int H, int dk, int dv, int num_seqs, int dtype);
+
+int kda_la_chunk_backward(const void *q, const void *k, const void *v, const float *log_decay,
+                          const float *init_state, const void *d_o, const float *dfinal_state, void *dq,
+                          void *dk_out, void *dv_out, float *dinit_state, const int32_t *cu_seqlens, int B, int T,
+                          int H, int dk, int dv, int num_seqs, int dtype, void *workspace, size_t ws_bytes,
+                          void *stream);
+
+/*
+ * Group norm with an activation, channels last: the norm between such a layer's
+ * heads and its output projection (one group per head: x = o as [B T, 1, H dv],
+ * G = H), or of any [N, L, C] tensor.
+ *
+ *     xhat = (x - mean) / sqrt(var + eps)     over the L positions and C / G channels of a group
+ *     z = xhat weight + bias;   y = act(z), or z act(gate) with a gate
+ *
+ *   x, gate, y    [N, L, C] in dtype, dense, 16-byte aligned; gate may be NULL
+ *   weight, bias  fp32 [C], 4-byte aligned, or NULL (ones, zeros)
+ *   mean, rstd    fp32 [N, G], written (the backward call reads them)
+ *   act           KDA_ACT_*;  eps > 0;  C a multiple of G
+ *   workspace     kda_group_norm_workspace_size() bytes, 256-byte aligned (0: may be NULL)
+ * N = 0 is a no-op.  Statistics and arithmetic are fp32, y is rounded once.
+ */
+#define KDA_ACT_NONE 0
+#define KDA_ACT_SILU 1
+#define KDA_ACT_SIGMOID 2
+
+size_t kda_group_norm_workspace_size(long long N, int L, int C, int G, int dtype, int backward);
+
+int kda_group_norm_forward(const void *x, const float *weight, const float *bias, const void *gate, void *y,
+                           float *mean, float *rstd, long long N, int L, int C, int G, float eps, int act,
+                           int dtype, void *workspace, size_t ws_bytes, void *stream);
+
+/* Gradients of sum <dy, y>: dx and dgate (required with a gate) in dtype, dweight and
+ * dbias fp32 [C] (each may be NULL), overwritten.  The same sums in the same order every time. */
+int kda_group_norm_backward(const void *dy, const void *x, const float *mean, const float *rstd,
+                            const float *weight, const float *bias, const void *gate, void *dx, void *dgate,
+                            float *dweight, float *dbias, long long N, int L, int C, int G, int act, int dtype,
+                            void *workspace, size_t ws_bytes, void *stream);
+
 /* Message for the calling thread's last non-OK return ("" if none). */
 const char *kda_last_error(void);
 
