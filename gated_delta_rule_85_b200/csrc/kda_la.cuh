@@ -127,10 +127,8 @@ struct Carry {
 // Joins the cut parts: thread = four elements of the state; CTA column w (blockIdx.x < W)
 // follows the sequence that goes on behind span w from span to span.  The sums are
 // independent loads, fetched kAhead spans ahead of the recurrence that adds them up.
-// WANT_LAST: the part in the span where the sequence ends has a sum too, and `last` is
-// written here; without it the walk writes it.  Columns W.. (packed): one sequence each,
-// handed through when it has no tokens.
-template <int C, int DIR, bool WANT_LAST>
+// Columns W.. (packed): one sequence each, handed through when it has no tokens.
+template <int C, int DIR>
 __global__ void __launch_bounds__(256) la_join_kernel(Geo g, Carry y, const float *__restrict__ log_decay, int E,
                                                       const int32_t *__restrict__ slots, int num_slots) {
     const int e = (blockIdx.y * 256 + threadIdx.x) * 4;   // E is a multiple of 1024
@@ -170,7 +168,7 @@ __global__ void __launch_bounds__(256) la_join_kernel(Geo g, Carry y, const floa
     float4 s = add(decay2(lg, (double)begun), s0, load4(y.sum_out + (long long)w * E + e));
     w += DIR;
     store4(y.start + (long long)w * E + e, s);
-    // spans that the sequence crosses from edge to edge, then the one it ends in
+    // spans that the sequence crosses from edge to edge
     constexpr int kAhead = 8;
     auto crossed = [&](int x) { return DIR > 0 ? u_last >= g.hi(x) : u_last < g.lo(x); };
     while (crossed(w)) {
@@ -191,11 +189,6 @@ __global__ void __launch_bounds__(256) la_join_kernel(Geo g, Carry y, const floa
                 w += DIR;
                 store4(y.start + (long long)w * E + e, s);
             }
-    }
-    if (WANT_LAST && y.last && row >= 0) {
-        const long long left = DIR > 0 ? cur.t1 - (cur.t0 + (g.lo(w) - u_first) * C)
-                                       : (g.hi(w) - u_last) * (long long)C;
-        store4(y.last + off, add(decay2(lg, (double)left), s, load4(y.sum_in + (long long)w * E + e)));
     }
 }
 

@@ -16,6 +16,7 @@
 #include "kda_bwd_tc.cuh"
 #include "kda_la.cuh"
 #include "kda_la_simt.cuh"
+#include "kda_la_tc.cuh"
 #include "kda_la_step.cuh"
 #include "kda_norm.cuh"
 
@@ -518,7 +519,7 @@ int la_forward(const kda::la::Call &c, const void *q, const void *k, const void 
 #define KDA_LA(DK, DV)                                                                                          \
     if (dk == DK && dv == DV)                                                                                   \
         e = dtype == KDA_BF16                                                                                   \
-                ? kda::la::simt_forward<DK, DV, __nv_bfloat16>(c, q, k, v, s0, o, last, (float *)ws)            \
+                ? kda::la::tc_forward<DK, DV>(c, q, k, v, s0, o, last, (float *)ws)                              \
                 : kda::la::simt_forward<DK, DV, float>(c, q, k, v, s0, o, last, (float *)ws)
     KDA_LA(64, 64);
     KDA_LA(64, 128);
@@ -929,8 +930,8 @@ int kda_la_chunk_backward(const void *q, const void *k, const void *v, const flo
 #define KDA_LA(DK, DV)                                                                                             \
     if (dk == DK && dv == DV)                                                                                      \
         e = dtype == KDA_BF16                                                                                      \
-                ? kda::la::simt_backward<DK, DV, __nv_bfloat16>(c, q, k, v, d_o, init_state, dfinal_state, dq, dk_out, \
-                                                                dv_out, dinit_state, (float *)workspace)           \
+                ? kda::la::tc_backward<DK, DV>(c, q, k, v, d_o, init_state, dfinal_state, dq, dk_out, dv_out,      \
+                                               dinit_state, (float *)workspace)                                   \
                 : kda::la::simt_backward<DK, DV, float>(c, q, k, v, d_o, init_state, dfinal_state, dq, dk_out, dv_out, \
                                                         dinit_state, (float *)workspace)
     KDA_LA(64, 64);
