@@ -1021,15 +1021,15 @@ inline EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// [tokens, H, inner] row-major tensor -> box (box_inner, 1, 64 tokens).
+// [tokens, H, inner] row-major tensor -> box (box_inner, 1, box_tokens).
 inline bool make_tmap(CUtensorMap *m, const void *base, CUtensorMapDataType dt, int esize, long long tokens,
                       int H, int inner, int box_inner,
-                      CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE) {
+                      CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE, int box_tokens = C) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)H, (cuuint64_t)tokens};
     cuuint64_t strides[2] = {(cuuint64_t)inner * esize, (cuuint64_t)inner * esize * H};
-    cuuint32_t box[3] = {(cuuint32_t)box_inner, 1u, (cuuint32_t)C};
+    cuuint32_t box[3] = {(cuuint32_t)box_inner, 1u, (cuuint32_t)box_tokens};
     cuuint32_t estr[3] = {1u, 1u, 1u};
     return fn(m, dt, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
               swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -126,9 +126,13 @@ struct Carry {
 
 // Joins the cut parts: thread = four elements of the state; CTA column w (blockIdx.x < W)
 // follows the sequence that goes on behind span w from span to span.  The sums are
-// independent loads, fetched kAhead spans ahead of the recurrence that adds them up.
-// Columns W.. (packed): one sequence each, handed through when it has no tokens.
-template <int C, int DIR>
+// independent loads, fetched kAhead spans ahead of the recurrence that adds them up, and the
+// decays of 32 spans at a time are one warp's work (fp64 exponentials by every thread took
+// longer than the loads: 14 us of a 196 us prefill).
+// WANT_LAST: the part in the span where the sequence ends has a sum too, and `last` is
+// written here; without it the walk writes it.  Columns W.. (packed): one sequence each,
+// handed through when it has no tokens.
+template <int C, int DIR, bool WANT_LAST>
 __global__ void __launch_bounds__(256) la_join_kernel(Geo g, Carry y, const float *__restrict__ log_decay, int E,
                                                       const int32_t *__restrict__ slots, int num_slots) {
     const int e = (blockIdx.y * 256 + threadIdx.x) * 4;   // E is a multiple of 1024
@@ -155,40 +159,71 @@ __global__ void __launch_bounds__(256) la_join_kernel(Geo g, Carry y, const floa
     const long long u_first = DIR > 0 ? edge - cur.c : edge + (cur.nck - 1 - cur.c);
     if (DIR > 0 ? u_first < lo : u_first >= hi) return;
     const long long u_last = DIR > 0 ? u_first + cur.nck - 1 : u_first - (cur.nck - 1);
-    const float lg = log_decay[cur.h];
     const int row = state_row(slots, num_slots, cur.n);
     const long long off = ((long long)max(row, 0) * g.H + cur.h) * E + e;
     const float4 s0 = row >= 0 && y.s0 ? load4(y.s0 + off) : zero;
+    const float4 out0 = load4(y.sum_out + (long long)w * E + e);
     if (y.s0_copy) store4(y.s0_copy + ((long long)cur.n * g.H + cur.h) * E + e, s0);
     auto add = [](float2 d, float4 s, float4 u) {
         return make_float4(fmaf(d.x, s.x, fmaf(d.y, s.x, u.x)), fmaf(d.x, s.y, fmaf(d.y, s.y, u.y)),
                            fmaf(d.x, s.z, fmaf(d.y, s.z, u.z)), fmaf(d.x, s.w, fmaf(d.y, s.w, u.w)));
     };
-    const long long begun = DIR > 0 ? (long long)(cur.c + 1) * C : cur.t1 - cur.tok();   // tokens so far
-    float4 s = add(decay2(lg, (double)begun), s0, load4(y.sum_out + (long long)w * E + e));
+    // spans behind w that the sequence crosses from edge to edge; in the next one it ends
+    auto crossed = [&](int x) { return x >= 0 && x < g.W && (DIR > 0 ? u_last >= g.hi(x) : u_last < g.lo(x)); };
+    const int w0 = w;
+    // tokens of the sequence in span x
+    auto tokens = [&](int x) -> double {
+        if (x == w0) return DIR > 0 ? (double)(cur.c + 1) * C : (double)(cur.t1 - cur.tok());
+        if (crossed(x)) return (double)(g.hi(x) - g.lo(x)) * C;
+        return DIR > 0 ? (double)(cur.t1 - (cur.t0 + (g.lo(x) - u_first) * C)) : (double)(g.hi(x) - u_last) * C;
+    };
+    __shared__ float2 dec[32];   // of the spans from `base` on
+    int base = 0;
+    auto decays = [&]() {
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            const int x = w0 + (base + (int)threadIdx.x) * DIR;
+            // behind the span where the sequence ends nothing is asked for
+            dec[threadIdx.x] = threadIdx.x + base > 0 && !crossed(x - DIR) && x - DIR != w0
+                                   ? make_float2(0.f, 0.f)
+                                   : decay2(log_decay[cur.h], tokens(x));
+        }
+        __syncthreads();
+    };
+    decays();
+    float4 s = add(dec[0], s0, out0);
+    int i = 1;
     w += DIR;
     store4(y.start + (long long)w * E + e, s);
-    // spans that the sequence crosses from edge to edge
     constexpr int kAhead = 8;
-    auto crossed = [&](int x) { return DIR > 0 ? u_last >= g.hi(x) : u_last < g.lo(x); };
     while (crossed(w)) {
         float4 u[kAhead];
         int m = 0;
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int x = w + i * DIR;
-            if (m == i && x >= 0 && x < g.W && crossed(x)) {
-                u[i] = load4(y.sum_in + (long long)x * E + e);
-                m = i + 1;
+        for (int k = 0; k < kAhead; ++k)
+            if (m == k && crossed(w + k * DIR)) {
+                u[k] = load4(y.sum_in + (long long)(w + k * DIR) * E + e);
+                m = k + 1;
             }
-        }
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (i < m) {
-                s = add(decay2(lg, (double)(g.hi(w) - g.lo(w)) * C), s, u[i]);
+        for (int k = 0; k < kAhead; ++k)
+            if (k < m) {
+                if (i - base == 32) {
+                    base = i;
+                    decays();
+                }
+                s = add(dec[i - base], s, u[k]);
+                ++i;
                 w += DIR;
                 store4(y.start + (long long)w * E + e, s);
             }
+    }
+    if (WANT_LAST && y.last && row >= 0) {
+        if (i - base == 32) {
+            base = i;
+            decays();
+        }
+        store4(y.last + off, add(dec[i - base], s, load4(y.sum_in + (long long)w * E + e)));
     }
 }
 

@@ -298,10 +298,10 @@ inline Carry carry_at(float *ws, int W, int E) {
     return y;
 }
 
-template <int C, int DIR>
+template <int C, int DIR, bool WANT_LAST>
 cudaError_t launch_join(const Geo &g, const Carry &y, const Call &c, int E) {
     const dim3 grid(g.W + (g.cu ? g.N : 0), E / 1024);
-    la_join_kernel<C, DIR><<<grid, 256, 0, c.st>>>(g, y, c.log_decay, E, c.slots, c.num_slots);
+    la_join_kernel<C, DIR, WANT_LAST><<<grid, 256, 0, c.st>>>(g, y, c.log_decay, E, c.slots, c.num_slots);
     return cudaGetLastError();
 }
 
@@ -328,7 +328,7 @@ cudaError_t simt_forward(const Call &c, const void *q, const void *k, const void
     cudaError_t e;
     if (cuts<kSimtC>(g)) {
         if ((e = launch_simt<DK, DV, Tin, 1, false>(g, wk, c)) != cudaSuccess) return e;
-        if ((e = launch_join<kSimtC, 1>(g, wk.y, c, DK * DV)) != cudaSuccess) return e;
+        if ((e = launch_join<kSimtC, 1, false>(g, wk.y, c, DK * DV)) != cudaSuccess) return e;
     }
     return launch_simt<DK, DV, Tin, 1, true>(g, wk, c);
 }
@@ -348,8 +348,8 @@ cudaError_t simt_backward(const Call &c, const void *q, const void *k, const voi
     if (cuts<kSimtC>(g)) {
         if ((e = launch_simt<DK, DV, Tin, 1, false>(g, sum_f, c)) != cudaSuccess) return e;
         if ((e = launch_simt<DK, DV, Tin, -1, false>(g, sum_b, c)) != cudaSuccess) return e;
-        if ((e = launch_join<kSimtC, 1>(g, fwd, c, E)) != cudaSuccess) return e;
-        if ((e = launch_join<kSimtC, -1>(g, bwd, c, E)) != cudaSuccess) return e;
+        if ((e = launch_join<kSimtC, 1, false>(g, fwd, c, E)) != cudaSuccess) return e;
+        if ((e = launch_join<kSimtC, -1, false>(g, bwd, c, E)) != cudaSuccess) return e;
     }
     Carry bwd_t = bwd;
     bwd_t.last = nullptr;

@@ -13,7 +13,8 @@
 // number, so it is split into bf16 terms that are multiplied in turn into one fp32
 // accumulator: three terms (24 bits) where the sum becomes a state that the caller gets or
 // another span starts from, two (16 bits, far inside the rounding of the state that rows
-// read) elsewhere.
+// read) elsewhere.  So the walk takes three terms only for sequences that lie in one span;
+// the states of cut ones are made by the first pass and the join.
 #pragma once
 
 #include "kda_chunk_tc.cuh"
@@ -26,46 +27,90 @@ namespace la {
 constexpr int kC = 128;                  // tokens of a chunk
 constexpr int kBox = 64;                 // token rows of a TMA box
 constexpr int kSumThreads = 320;         // producer warp, MMA warp, eight compute warps
-constexpr int kWalkThreads = 448;        // producer, MMA, four output warps, eight state warps
+constexpr int kStateWarps = 8;
+constexpr int kWalkThreads = 192 + kStateWarps * 32;   // producer, MMA, four output warps, state warps
+constexpr int kOutBox = 32;              // token rows of an output box: one warp's
 
 // Waits are bounded, and a warp gives up as a whole.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, parity, kda::tc::WAIT_LIMIT_CYCLES));
+    return __all_sync(0xffffffffu, ptx::mbar_wait_tries(bar, parity));
+}
+// One warp of a group polls, the others sleep on a hardware barrier: polling warps take issue
+// slots from working ones (measured: more instructions than the work itself).  The barrier also
+// hands round whether the poll succeeded, so that no warp is left waiting.
+template <int ID, int THREADS>
+__device__ __forceinline__ bool wait_group(bool leader, uint32_t bar, uint32_t parity) {
+    uint32_t ok = 1;
+    if (leader) ok = wait_warp(bar, parity);
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %0, 0;\n\t"
+        "barrier.cta.red.and.pred p, %1, %2, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "+r"(ok)
+        : "n"(ID), "n"(THREADS)
+        : "memory");
+    return ok != 0;
 }
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ float lo_bf16(uint32_t x) { return __uint_as_float(x << 16); }
-__device__ __forceinline__ float hi_bf16(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 // 16-byte group g of row r in a 128-byte-swizzled atom (64 bf16 wide)
 __device__ __forceinline__ uint32_t swz(int r, int g) { return (uint32_t)(r * 128 + ((g ^ (r & 7)) << 4)); }
 
-// Eight weighted elements as bf16 terms: w x = t0 + t1 (+ t2), each the rounding of what is left.
+// A weight as bf16 terms that sum to it (24 bits), each twice.
+struct Weight {
+    __nv_bfloat162 w0, w1, w2;
+    __device__ __forceinline__ explicit Weight(float w) {
+        const float a = __bfloat162float(__float2bfloat16_rn(w)), b = __bfloat162float(__float2bfloat16_rn(w - a));
+        w0 = __float2bfloat162_rn(a);
+        w1 = __float2bfloat162_rn(b);
+        w2 = __float2bfloat162_rn(w - a - b);
+    }
+};
+
+// Eight weighted elements as bf16 terms, largest first, in bf16 arithmetic two at a time (a
+// third of the instructions of the same in fp32, and no conversions).  A product of two bf16
+// numbers is the sum of its rounding and a residual that fused multiply-add gives exactly:
+//   w0 x = t0 + r,  w1 x = p + q,  t1 = round(r + p),  t2 = (r + p - t1) + q + w2 x
+// with r + p - t1 exact by the two-sum.  What is dropped is below 2^-25 of w x; with two
+// terms, t1 = round(w1 x + r), below 2^-16.
 template <bool THREE>
-__device__ __forceinline__ void split8(const uint4 &x, float w, uint4 &t0, uint4 &t1, uint4 &t2) {
+__device__ __forceinline__ void split8(const uint4 &x, const Weight &w, uint4 &t0, uint4 &t1, uint4 &t2) {
     const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-    uint32_t o0[4], o1[4], o2[4];
+    uint32_t o[3][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float a = lo_bf16(in[i]) * w, b = hi_bf16(in[i]) * w;
-        o0[i] = pack2(a, b);
-        const float a1 = a - lo_bf16(o0[i]), b1 = b - hi_bf16(o0[i]);
-        o1[i] = pack2(a1, b1);
-        o2[i] = THREE ? pack2(a1 - lo_bf16(o1[i]), b1 - hi_bf16(o1[i])) : 0u;
+        const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162 *>(&in[i]);
+        const __nv_bfloat162 a = __hmul2_rn(w.w0, v), r = __hfma2(w.w0, v, __hneg2(a));
+        __nv_bfloat162 b, c = __nv_bfloat162();
+        if (THREE) {
+            const __nv_bfloat162 p = __hmul2_rn(w.w1, v), q = __hfma2(w.w1, v, __hneg2(p));
+            b = __hadd2_rn(r, p);
+            const __nv_bfloat162 z = __hsub2_rn(b, r);
+            const __nv_bfloat162 e = __hadd2_rn(__hsub2_rn(r, __hsub2_rn(b, z)), __hsub2_rn(p, z));
+            c = __hadd2_rn(e, __hfma2(w.w2, v, q));
+        } else {
+            b = __hfma2(w.w1, v, r);
+        }
+        o[0][i] = *reinterpret_cast<const uint32_t *>(&a);
+        o[1][i] = *reinterpret_cast<const uint32_t *>(&b);
+        o[2][i] = *reinterpret_cast<const uint32_t *>(&c);
     }
-    t0 = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-    t1 = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-    t2 = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+    t0 = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
+    t1 = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
+    t2 = make_uint4(o[2][0], o[2][1], o[2][2], o[2][3]);
 }
 
 // ------------------------------------------------------------------ first pass
 
-// The sum of b c^T over the part of a sequence that lies in a span and goes on behind it
-// (in walking order): sum_out, or sum_in when the sequence came from the span before.
-// Only the sequence at the span's far edge can have such a part, and its tokens are
-// contiguous: the CTA runs over them in tiles of 64 from the far edge towards the near
-// one, against the walk, so that what the walk reads first is what L2 saw last.
+// Sums of b c^T over the parts of cut sequences that lie in a span: of the one that goes on
+// behind the span in walking order (sum_out, or sum_in when it came from the span before
+// too), and with final states wanted of the one that came from before and ends in it
+// (sum_in).  The tokens of a part are contiguous: the CTA runs over them in tiles of 64 from
+// the far end towards the near one, against the walk, and takes the far part first, so that
+// what the walk reads first is what L2 saw last.
 //
 // A tile's three-term products leave TMEM after 12 K steps and are added in fp32 registers,
 // scaled by the decay of the tokens behind the tile, so that neither the tensor core's
@@ -74,6 +119,7 @@ struct SumRole {
     CUtensorMap b, c;
     float *sum_in, *sum_out;
     int dir;
+    int want_last;
 };
 struct SumArgs {
     SumRole role[2];
@@ -105,19 +151,48 @@ la_sum_kernel(const __grid_constant__ SumArgs args, Geo g, const float *__restri
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const SumRole &role = args.role[blockIdx.y];
     const int dir = role.dir, w = blockIdx.x;
-    const long long lo = g.lo(w), hi = g.hi(w), edge = dir > 0 ? hi - 1 : lo;
-    Cursor<kC> cur;
-    cur.seek(g, edge);
-    if (!cur.valid || cur.c == (dir > 0 ? cur.nck - 1 : 0)) return;   // nothing goes on behind the span
-    // the part's tokens [ta, tb); did its sequence come from the span before?
-    const long long u_near = dir > 0 ? edge - cur.c : edge + (cur.nck - 1 - cur.c);
-    const bool through = dir > 0 ? u_near < lo : u_near >= hi;
-    const long long near = through ? (dir > 0 ? lo : hi - 1) : u_near;
-    const long long ta = dir > 0 ? cur.tok() - (edge - near) * kC : cur.tok();
-    const long long tb = dir > 0 ? cur.tok() + kC : min(cur.t1, cur.tok() + (near - edge + 1) * kC);
-    const int nt = (int)((tb - ta + kBox - 1) / kBox);
-    // tile x counts from the far edge; only a sequence's last tile can be shorter than 64
-    auto tile_tok = [&](int x) { return ta + (long long)(dir > 0 ? nt - 1 - x : x) * kBox; };
+    const long long lo = g.lo(w), hi = g.hi(w);
+    // the far part, then the near one: tokens [ta, tb) in nt tiles, counted from the far end
+    struct Part {
+        long long ta, tb;
+        int h, nt;
+        bool in;   // came from the span before
+    } part[2];
+    part[0] = part[1] = Part{0, 0, 0, 0, false};
+    {
+        Cursor<kC> cur;
+        const long long edge = dir > 0 ? hi - 1 : lo;
+        cur.seek(g, edge);
+        bool through = false;
+        if (cur.valid && cur.c != (dir > 0 ? cur.nck - 1 : 0)) {
+            const long long u_near = dir > 0 ? edge - cur.c : edge + (cur.nck - 1 - cur.c);
+            through = dir > 0 ? u_near < lo : u_near >= hi;
+            const long long near = through ? (dir > 0 ? lo : hi - 1) : u_near;
+            Part &p = part[0];
+            p.ta = dir > 0 ? cur.tok() - (edge - near) * kC : cur.tok();
+            p.tb = dir > 0 ? cur.tok() + kC : min(cur.t1, cur.tok() + (near - edge + 1) * kC);
+            p.h = cur.h;
+            p.in = through;
+        }
+        if (role.want_last && !through) {
+            cur.seek(g, dir > 0 ? lo : hi - 1);
+            // it came from before, and its end (all of it that is left) lies in the span
+            const int left = dir > 0 ? cur.nck - 1 - cur.c : cur.c;
+            if (cur.valid && cur.c != (dir > 0 ? 0 : cur.nck - 1) && left < hi - lo) {
+                Part &p = part[1];
+                p.ta = dir > 0 ? cur.tok() : cur.t0;
+                p.tb = dir > 0 ? cur.t1 : min(cur.t1, cur.tok() + kC);
+                p.h = cur.h;
+                p.in = true;
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) part[x].nt = (int)((part[x].tb - part[x].ta + kBox - 1) / kBox);
+    }
+    const int nt = part[0].nt + part[1].nt;
+    if (nt == 0) return;   // nothing cut
+    // first token of tile x; only a part's last tile in time can be shorter than 64
+    auto tile_tok = [&](const Part &p, int x) { return p.ta + (long long)(dir > 0 ? p.nt - 1 - x : x) * kBox; };
 
     if (warp == 1) {
         ptx::tmem_alloc(ptx::smem_u32(tslot), 256);
@@ -147,13 +222,15 @@ la_sum_kernel(const __grid_constant__ SumArgs args, Geo g, const float *__restri
             if (n >= NST && !(ok = wait_warp(bar_done + 8 * s, (uint32_t)((n / NST - 1) & 1)))) break;
             if (lane == 0) {
                 const uint32_t bar = bar_full + 8 * s, dst = sb + s * L::STAGE;
-                const int t = (int)tile_tok(n);
+                const bool far = n < part[0].nt;
+                const Part &p = far ? part[0] : part[1];
+                const int t = (int)tile_tok(p, far ? n : n - part[0].nt);
                 ptx::mbar_arrive_expect_tx(bar, L::STAGE);
 #pragma unroll
-                for (int a = 0; a < DB / 64; ++a) ptx::tma_load_3d(dst + a * 8192, &role.b, bar, a * 64, cur.h, t);
+                for (int a = 0; a < DB / 64; ++a) ptx::tma_load_3d(dst + a * 8192, &role.b, bar, a * 64, p.h, t);
 #pragma unroll
                 for (int a = 0; a < DC / 64; ++a)
-                    ptx::tma_load_3d(dst + L::BT + a * 8192, &role.c, bar, a * 64, cur.h, t);
+                    ptx::tma_load_3d(dst + L::BT + a * 8192, &role.c, bar, a * 64, p.h, t);
             }
             __syncwarp();
         }
@@ -198,16 +275,11 @@ la_sum_kernel(const __grid_constant__ SumArgs args, Geo g, const float *__restri
         const int jr = ct & 63, jq = ct >> 6;     // split: token row, quarter of the columns
         const int row = quad * 32 + lane, col = half * CPT;
         const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16) + col;
+        auto wait_sum = [&](uint32_t bar, uint32_t parity) { return wait_group<1, 256>(warp == 2, bar, parity); };
         float S[CPT];
-#pragma unroll
-        for (int x = 0; x < CPT; ++x) S[x] = 0.f;
-        const double lg = (double)log_decay[cur.h];
-        const double full_dec = exp(lg * kBox);
-        const float full_wt = (float)exp(lg * (dir > 0 ? kBox - 1 - jr : jr + 1));
-        double behind = 1.0;         // decay of the tokens behind the tile
-        float scale[2];              // the same for the two tiles in flight
+        float scale[2] = {};         // decay of the tokens behind the two tiles in flight
         auto drain = [&](int x) {    // adds tile x's sum
-            if (!(ok = wait_warp(bar_done + 8 * (x % NST), (uint32_t)((x / NST) & 1)))) return;
+            if (!(ok = wait_sum(bar_done + 8 * (x % NST), (uint32_t)((x / NST) & 1)))) return;
             ptx::tc_fence_after();
             if (quad * 32 < DB) {
                 const uint32_t u = tl + (x & 1) * 128;
@@ -222,47 +294,62 @@ la_sum_kernel(const __grid_constant__ SumArgs args, Geo g, const float *__restri
                 }
             }
         };
-        for (int n = 0; n < nt; ++n) {
-            const int s = n % NST, e = n & 1;
-            // the middle and low terms' buffer is free: tile n - 2 was drained
-            if (!(ok = wait_warp(bar_full + 8 * s, (uint32_t)((n / NST) & 1)))) break;
-            const int len = (int)min((long long)kBox, tb - tile_tok(n));
-            uint8_t *bt = sm + s * L::STAGE, *c0 = bt + L::BT;
-            uint8_t *c1 = sm + L::E + e * 2 * L::CT, *c2 = c1 + L::CT;
-            const bool live = jr < len;
-            // forwards a part ends with a full chunk; backwards the weight counts from the tile's start
-            const float wt = full_wt;
+        int n = 0;
+#pragma unroll 1
+        for (int q = 0; q < 2 && ok; ++q) {
+            const Part &p = part[q];
+            if (p.nt == 0) continue;
 #pragma unroll
-            for (int k = 0; k < DC / 32; ++k) {
-                const int cg = jq * (DC / 32) + k;   // 16-byte group of the row
-                const uint32_t at = (cg >> 3) * 8192 + swz(jr, cg & 7);
-                uint4 t0 = make_uint4(0, 0, 0, 0), t1 = t0, t2 = t0;   // rows behind the end may hold anything
-                if (live) split8<true>(*reinterpret_cast<const uint4 *>(c0 + at), wt, t0, t1, t2);
-                *reinterpret_cast<uint4 *>(c0 + at) = t0;
-                *reinterpret_cast<uint4 *>(c1 + at) = t1;
-                *reinterpret_cast<uint4 *>(c2 + at) = t2;
-            }
-            if (!live)
+            for (int x = 0; x < CPT; ++x) S[x] = 0.f;
+            const double lg = (double)log_decay[p.h];
+            const double full_dec = exp(lg * kBox);
+            double behind = 1.0;
+            // forwards the weight counts from the tile's end, backwards from its start
+            const Weight full_wt((float)exp(lg * (dir > 0 ? kBox - 1 - jr : jr + 1)));
+#pragma unroll 1
+            for (int x = 0; x < p.nt; ++x, ++n) {
+                const int s = n % NST, e = n & 1;
+                // the middle and low terms' buffer is free: tile n - 2 was drained
+                if (!(ok = wait_sum(bar_full + 8 * s, (uint32_t)((n / NST) & 1)))) break;
+                const int len = (int)min((long long)kBox, p.tb - tile_tok(p, x));
+                const uint32_t bt = sb + s * L::STAGE, c0 = bt + L::BT;
+                const uint32_t c1 = sb + L::E + e * 2 * L::CT, c2 = c1 + L::CT;
+                const bool live = jr < len;
+                Weight wt = full_wt;
+                if (len < kBox && dir > 0) wt = Weight(live ? (float)exp(lg * (len - 1 - jr)) : 0.f);
 #pragma unroll
-                for (int k = 0; k < DB / 32; ++k) {
-                    const int cg = jq * (DB / 32) + k;
-                    *reinterpret_cast<uint4 *>(bt + (cg >> 3) * 8192 + swz(jr, cg & 7)) = make_uint4(0, 0, 0, 0);
+                for (int k = 0; k < DC / 32; ++k) {
+                    const int cg = jq * (DC / 32) + k;   // 16-byte group of the row
+                    const uint32_t at = (cg >> 3) * 8192 + swz(jr, cg & 7);
+                    uint4 t0 = make_uint4(0, 0, 0, 0), t1 = t0, t2 = t0;   // rows behind the end may hold anything
+                    if (live) split8<true>(ptx::lds128(c0 + at), wt, t0, t1, t2);
+                    ptx::sts128(c0 + at, t0);
+                    ptx::sts128(c1 + at, t1);
+                    ptx::sts128(c2 + at, t2);
                 }
-            if (e) scale[1] = (float)behind;
-            else scale[0] = (float)behind;
-            behind *= full_dec;
-            ptx::fence_proxy_async_smem();
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar_ready + 8 * e);
-            if (n > 0) drain(n - 1);   // the tile before, while this one multiplies
-            if (!ok) break;
-        }
-        if (ok) drain(nt - 1);
-        if (ok && row < DB) {
-            float *dst = (through ? role.sum_in : role.sum_out) + ((long long)w * DB + row) * DC + col;
+                if (!live)
 #pragma unroll
-            for (int x = 0; x < CPT; x += 4) store4(dst + x, make_float4(S[x], S[x + 1], S[x + 2], S[x + 3]));
+                    for (int k = 0; k < DB / 32; ++k) {
+                        const int cg = jq * (DB / 32) + k;
+                        ptx::sts128(bt + (cg >> 3) * 8192 + swz(jr, cg & 7), 0, 0, 0, 0);
+                    }
+                if (e) scale[1] = (float)behind;
+                else scale[0] = (float)behind;
+                behind *= len == kBox ? full_dec : exp(lg * len);
+                ptx::fence_proxy_async_smem();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar_ready + 8 * e);
+                if (x > 0) drain(n - 1);   // the tile before, while this one multiplies
+                if (!ok) break;
+            }
+            if (!ok) break;
+            drain(n - 1);
+            if (ok && row < DB) {
+                float *dst = (p.in ? role.sum_in : role.sum_out) + ((long long)w * DB + row) * DC + col;
+#pragma unroll
+                for (int x = 0; x < CPT; x += 4) store4(dst + x, make_float4(S[x], S[x + 1], S[x + 2], S[x + 3]));
+            }
         }
         if (!ok && lane == 0) flag_status(KDA_DEV_WAIT_TIMEOUT);
     }
@@ -284,6 +371,7 @@ struct SpanWalk {
     bool ends;              // the item is the last of its sequence in walking order
     bool first;             // the first item of a part
     bool from_before;       // its part's sequence started in an earlier span
+    bool whole;             // its sequence lies in this span from start to end
     bool fresh;
 
     __device__ __forceinline__ SpanWalk(const Geo &g, int w, int dir_) : lo(g.lo(w)), hi(g.hi(w)), i(-1), dir(dir_) {
@@ -303,19 +391,20 @@ struct SpanWalk {
             ends = cur.c == (dir > 0 ? cur.nck - 1 : 0);
             from_before = fresh && !begins;
             first = fresh || begins;
+            if (first) whole = begins && (dir > 0 ? cur.nck - 1 - cur.c : cur.c) < hi - lo - i;
             fresh = false;
             return true;
         }
         return false;
     }
-    // items of the sequence behind this one lie in the span too, all of them or some
-    __device__ __forceinline__ int left() const { return dir > 0 ? cur.nck - 1 - cur.c : cur.c; }
-    __device__ __forceinline__ bool whole_tail() const { return left() < hi - lo - i; }
-    __device__ __forceinline__ bool part_over() const { return ends || i == hi - lo - 1; }
+    // the chunk's U is needed: by the part's next chunk, or for a final state that the walk writes
+    __device__ __forceinline__ bool need_u(bool want_last) const {
+        return !(ends || i == hi - lo - 1) || (ends && whole && want_last);
+    }
 };
 
 struct WalkRole {
-    CUtensorMap a, b, c;
+    CUtensorMap a, b, c, out_map;
     __nv_bfloat16 *out;
     Carry y;
     int dir;
@@ -337,7 +426,7 @@ struct WalkSmem {
     static constexpr int X = 0;
     static constexpr int ST0 = AT;
     static constexpr int BAR = ST0 + NST * STAGE;
-    static constexpr int BYTES = BAR + 8 * (2 * NST + 9) + 16;
+    static constexpr int BYTES = BAR + 8 * (3 * NST + 9) + 16;
     static constexpr int ALLOC = BYTES + 1024;
     static_assert(NST >= 2 && ALLOC <= 232448, "shared memory");
 };
@@ -361,10 +450,10 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sb = ptx::smem_u32(sm);
-    const uint32_t bar_full = sb + L::BAR, bar_free = bar_full + 8 * NST, bar_sc = bar_free + 8 * NST,
-                   bar_in = bar_sc + 8, bar_p = bar_in + 8, bar_b = bar_p + 8, bar_u = bar_b + 8, bar_o = bar_u + 8,
+    const uint32_t bar_full = sb + L::BAR, bar_free = bar_full + 8 * NST, bar_out = bar_free + 8 * NST,
+                   bar_sc = bar_out + 8 * NST, bar_in = bar_sc + 8, bar_p = bar_in + 8, bar_b = bar_p + 8, bar_u = bar_b + 8, bar_o = bar_u + 8,
                    bar_x = bar_o + 8, bar_od = bar_x + 8, bar_fin = bar_od + 8;
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::BAR + 8 * (2 * NST + 9));
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::BAR + 8 * (3 * NST + 9));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // the roles of one span run side by side: they share most of their tiles in L2
     const WalkRole &role = args.role[blockIdx.x % roles];
@@ -380,14 +469,15 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
         for (int s = 0; s < NST; ++s) {
             ptx::mbar_init(bar_full + 8 * s, 1);
             ptx::mbar_init(bar_free + 8 * s, 1);
+            ptx::mbar_init(bar_out + 8 * s, 4);
         }
         ptx::mbar_init(bar_sc, 1);
         ptx::mbar_init(bar_in, 1);
         ptx::mbar_init(bar_p, 4);
-        ptx::mbar_init(bar_b, 8);
+        ptx::mbar_init(bar_b, kStateWarps);
         ptx::mbar_init(bar_u, 1);
         ptx::mbar_init(bar_o, 1);
-        ptx::mbar_init(bar_x, 8);
+        ptx::mbar_init(bar_x, kStateWarps);
         ptx::mbar_init(bar_od, 4);
         ptx::mbar_init(bar_fin, 1);
         ptx::fence_mbar_init();
@@ -405,26 +495,32 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
         // ---------------- producer
         while (it.next(g)) {
             const int s = n % NST;
-            if (n >= NST && !(ok = wait_warp(bar_free + 8 * s, (uint32_t)((n / NST - 1) & 1)))) break;
+            const uint32_t bar = bar_full + 8 * s, dst = sb + L::ST0 + s * L::STAGE, old = (uint32_t)((n / NST - 1) & 1);
+            const int len = it.cur.len(), t = (int)it.cur.tok(), h = it.cur.h;
+            const int boxes = len > kBox ? 2 : 1;
+            auto load = [&](const CUtensorMap *map, uint32_t at, int atoms) {
+                for (int x = 0; x < boxes; ++x)
+                    for (int a = 0; a < atoms; ++a)
+                        ptx::tma_load_3d(at + a * 16384 + x * 8192, map, bar, a * 64, h, t + x * kBox);
+            };
+            // the last product frees C (and B); the tiles that the output goes through are free once it is out
+            constexpr bool B_EARLY = DC <= DAB;
+            if (n >= NST && !(ok = wait_warp(bar_free + 8 * s, old))) break;
             if (lane == 0) {
-                const uint32_t bar = bar_full + 8 * s, dst = sb + L::ST0 + s * L::STAGE;
-                const int len = it.cur.len(), t = (int)it.cur.tok(), h = it.cur.h;
-                const int boxes = len > kBox ? 2 : 1;
                 ptx::mbar_arrive_expect_tx(bar, (uint32_t)(L::STAGE / 2 * boxes));
-                for (int x = 0; x < boxes; ++x) {
-#pragma unroll
-                    for (int a = 0; a < DAB / 64; ++a) {
-                        const uint32_t at = dst + a * 16384 + x * 8192;
-                        ptx::tma_load_3d(at, &role.a, bar, a * 64, h, t + x * kBox);
-                        ptx::tma_load_3d(at + L::AT, &role.b, bar, a * 64, h, t + x * kBox);
-                    }
-#pragma unroll
-                    for (int a = 0; a < DC / 64; ++a)
-                        ptx::tma_load_3d(dst + 2 * L::AT + a * 16384 + x * 8192, &role.c, bar, a * 64, h, t + x * kBox);
-                }
+                if (B_EARLY) load(&role.b, dst + L::AT, DAB / 64);
+                load(&role.c, dst + 2 * L::AT, DC / 64);
+            }
+            __syncwarp();
+            ok = n < NST || wait_warp(bar_out + 8 * s, old);
+            // (after a wait that ran out the rest is loaded all the same: the barrier has counted it)
+            if (lane == 0) {
+                load(&role.a, dst, DAB / 64);
+                if (!B_EARLY) load(&role.b, dst + L::AT, DAB / 64);
             }
             __syncwarp();
             ++n;
+            if (!ok) break;
         }
         if (!ok) {
             if (lane == 0) flag_status(KDA_DEV_WAIT_TIMEOUT);
@@ -443,7 +539,7 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
             if (!ok) break;
             ptx::tc_fence_after();
             if (lane == 0) {
-#pragma unroll
+#pragma unroll 4
                 for (int ks = 0; ks < DAB / 16; ++ks)
                     ptx::mma_bf16(t_sc, kda::tc::kdesc(at, ks, kC), kda::tc::kdesc(bt, ks, kC), id_sc, ks > 0);
                 ptx::mma_commit(bar_sc);
@@ -453,7 +549,7 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
             if (!ok) break;
             ptx::tc_fence_after();
             if (lane == 0) {
-#pragma unroll
+#pragma unroll 4
                 for (int ks = 0; ks < DAB / 16; ++ks)
                     ptx::mma_bf16(t_oi, kda::tc::kdesc(at, ks, kC),
                                   ptx::desc_mnmajor_sw128(sb + L::X + ks * 2048, DAB * 128, 1024), id_in, ks > 0);
@@ -462,17 +558,18 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
             __syncwarp();
             if (!(ok = wait_warp(bar_b, ph))) break;
             ptx::tc_fence_after();
-            if (!it.part_over() || (it.ends && want_last)) {
+            if (it.need_u(want_last)) {
                 if (lane == 0) {
+                    const bool three = want_last && it.whole;
                     auto term = [&](uint32_t x, uint32_t acc) {
-#pragma unroll
+#pragma unroll 4
                         for (int ks = 0; ks < kC / 16; ++ks)
                             ptx::mma_bf16(t_u, ptx::desc_mnmajor_sw128(x + ks * 2048, 16384, 1024),
                                           ptx::desc_mnmajor_sw128(ct + ks * 2048, 16384, 1024), id_u, acc + ks > 0);
                     };
                     // small terms first: the accumulator is least rounded while it is small
-                    if (want_last) term(sb + L::X, 0);
-                    term(at, want_last ? 1 : 0);
+                    if (three) term(sb + L::X, 0);
+                    term(at, three ? 1 : 0);
                     term(bt, 1);
                     ptx::mma_commit(bar_u);
                 }
@@ -481,7 +578,7 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
             if (!(ok = wait_warp(bar_p, ph))) break;
             ptx::tc_fence_after();
             if (lane == 0) {
-#pragma unroll
+#pragma unroll 4
                 for (int ks = 0; ks < kC / 16; ++ks)
                     ptx::mma_bf16_ts(t_oa, t_sc + ks * 8, ptx::desc_mnmajor_sw128(ct + ks * 2048, 16384, 1024), id_in,
                                      ks > 0);
@@ -500,9 +597,14 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
     } else if (warp < 6) {
         // ---------------- scores -> P, accumulators -> out.  Thread <-> row i.
         const int quad = warp & 3, i = quad * 32 + lane;
+        auto wait_out = [&](uint32_t bar, uint32_t parity) { return wait_group<1, 128>(warp == 2, bar, parity); };
         const uint32_t tl = (uint32_t)(quad * 32) << 16;
-        float step[16];   // g^(15 - m) forwards, g^m backwards, m = 0..15
-        float l2 = 0.f;   // log2 g: P and out are rounded to bf16, which a fast exponential's error does not reach
+        // Powers that a head keeps: in a 16-column block all on one side of the diagonal
+        // g^|i-j| = g^(distance to the block's nearest column) step[m]; in the row's own block it is
+        // near[m].  P and out are rounded to bf16, which a fast exponential's error does not reach.
+        float step[16], near[16];
+        float l2 = 0.f;   // log2 g
+        const int li = i & 15, bi = i >> 4;
         int head = -1;
         while (it.next(g)) {
             const uint32_t ph = (uint32_t)(n & 1);
@@ -512,92 +614,122 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
                 head = h;
                 l2 = log_decay[h] * 1.44269504f;
 #pragma unroll
-                for (int m = 0; m < 16; ++m) step[m] = kda::tc::exp2_fast(l2 * (dir > 0 ? 15 - m : m));
+                for (int m = 0; m < 16; ++m) {
+                    step[m] = kda::tc::exp2_fast(l2 * (dir > 0 ? 15 - m : m));
+                    near[m] = kda::tc::exp2_fast(l2 * max((li - m) * dir, 0));
+                }
             }
-            if (!(ok = wait_warp(bar_sc, ph))) break;
+            if (!(ok = wait_out(bar_sc, ph))) break;
             ptx::tc_fence_after();
-            // 32 score columns a step.  In a 16-column block all on one side of the diagonal
-            // g^|i-j| = g^(distance to its nearest column) step[m]; on the diagonal each has its own.
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                uint32_t p[16];
-                if (dir > 0 ? b > quad : b < quad) {
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) p[x] = 0u;
-                } else {
-                    float s[32];
-                    ptx::tmem_ld32(t_sc + tl + 32 * b, s);
+            // 16 score columns a step (P overwrites scores that were read).  Loops over columns stay
+            // rolled here: the kernel's steady state has to fit the instruction cache.
+            const int open0 = dir > 0 ? 0 : 2 * quad + 2, open1 = dir > 0 ? 2 * quad : len >> 4;   // no row of the warp masked
+#pragma unroll 1
+            for (int b = 0; b < 8; ++b) {
+                uint32_t p[8];
+                if (b >= open0 && b < open1) {
+                    float s[16];
+                    ptx::tmem_ld16(t_sc + tl + 16 * b, s);
+                    const float r = kda::tc::exp2_fast(l2 * (dir > 0 ? i - 16 * b - 15 : 16 * b - i));
                     ptx::tmem_wait_ld();
-                    if (b != quad) {
+#pragma unroll
+                    for (int m = 0; m < 16; m += 2) {
+                        const float2 c = ptx::mul2(make_float2(step[m], step[m + 1]), make_float2(r, r));
+                        const float2 z = ptx::mul2(make_float2(s[m], s[m + 1]), c);
+                        p[m / 2] = pack2(z.x, z.y);
+                    }
+                } else if (dir > 0 ? b > 2 * quad + 1 : b < 2 * quad) {
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) p[x] = 0u;
+                } else {
+                    float s[16];
+                    ptx::tmem_ld16(t_sc + tl + 16 * b, s);
+                    // scores on the masked side and behind the end may be anything, and count as zeros
+                    const int side = (bi - b) * dir;   // 0: the row's own block, below: masked
+                    const int first = side == 0 && dir < 0 ? li : 0;
+                    const int last = side < 0 ? -1 : min(side == 0 && dir > 0 ? li : 15, len - 1 - 16 * b);
+                    const float r = kda::tc::exp2_fast(l2 * max(dir > 0 ? i - 16 * b - 15 : 16 * b - i, 0));
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int m = 0; m < 16; m += 2) {
+                        float c[2], z[2];
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const int j0 = 32 * b + 16 * k;
-                            const float r = kda::tc::exp2_fast(l2 * (dir > 0 ? i - j0 - 15 : j0 - i));
-#pragma unroll
-                            for (int m = 0; m < 16; ++m) s[16 * k + m] *= r * step[m];
+                            c[k] = side == 0 ? near[m + k] : step[m + k] * r;
+                            z[k] = m + k >= first && m + k <= last ? s[m + k] * c[k] : 0.f;
                         }
-                    } else {
-#pragma unroll
-                        for (int m = 0; m < 32; ++m) {
-                            const int d = (lane - m) * dir;
-                            s[m] = d >= 0 ? s[m] * kda::tc::exp2_fast(l2 * d) : 0.f;
-                        }
-                    }
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) p[x] = pack2(s[2 * x], s[2 * x + 1]);
-                    if (dir < 0 && 32 * b + 32 > len) {
-                        // backwards in time the masked side does not cover the rows behind the end
-#pragma unroll
-                        for (int x = 0; x < 16; ++x) {
-                            const int j = 32 * b + 2 * x;
-                            if (j >= len) p[x] = 0u;
-                            else if (j + 1 >= len) p[x] &= 0xffffu;
-                        }
+                        p[m / 2] = pack2(z[0], z[1]);
                     }
                 }
-                ptx::tmem_st16(t_sc + tl + 16 * b, p);
+                ptx::tmem_st8(t_sc + tl + 8 * b, p);
             }
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar_p);
-            if (!(ok = wait_warp(bar_o, ph))) break;
+            if (!(ok = wait_out(bar_o, ph))) break;
             ptx::tc_fence_after();
-            const float up = i < len ? kda::tc::exp2_fast(l2 * (dir > 0 ? i + 1 : len - 1 - i)) : 0.f;
-            __nv_bfloat16 *dst = role.out + ((t + i) * g.H + h) * DC;
-#pragma unroll
-            for (int b = 0; b < DC / 16; ++b) {
-                float oa[16], oi[16];
-                ptx::tmem_ld16(t_oa + tl + 16 * b, oa);
-                ptx::tmem_ld16(t_oi + tl + 16 * b, oi);
+            // the rows leave through the tile of A (and B): every product of the chunk is done
+            const float up = kda::tc::exp2_fast(l2 * (dir > 0 ? i + 1 : max(len - 1 - i, 0)));
+            const int s = n % NST;
+            const uint32_t tile = sb + L::ST0 + s * L::STAGE;
+#pragma unroll 1
+            for (int b = 0; b < DC / 32; ++b) {
+                float u[32], v[32];
+                ptx::tmem_ld32(t_oa + tl + 32 * b, u);
+                ptx::tmem_ld32(t_oi + tl + 32 * b, v);
                 ptx::tmem_wait_ld();
-                if (i < len) {
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        uint32_t r[4];
+                for (int x = 0; x < 4; ++x) {
+                    uint32_t r[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            r[k] = pack2(fmaf(up, oi[8 * x + 2 * k], oa[8 * x + 2 * k]),
-                                         fmaf(up, oi[8 * x + 2 * k + 1], oa[8 * x + 2 * k + 1]));
-                        *reinterpret_cast<uint4 *>(dst + 16 * b + 8 * x) = make_uint4(r[0], r[1], r[2], r[3]);
+                    for (int k = 0; k < 4; ++k) {
+                        const int e = 8 * x + 2 * k;
+                        const float2 z = ptx::fma2(make_float2(up, up), make_float2(v[e], v[e + 1]), make_float2(u[e], u[e + 1]));
+                        r[k] = pack2(z.x, z.y);
                     }
+                    const int cg = 4 * b + x;
+                    ptx::sts128(tile + (cg >> 3) * 16384 + swz(i, cg & 7), r[0], r[1], r[2], r[3]);
                 }
             }
             ptx::tc_fence_before();
+            ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar_od);
+            if (quad * 32 + 32 <= len) {
+                if (lane == 0) {
+#pragma unroll
+                    for (int a = 0; a < DC / 64; ++a)
+                        ptx::tma_store_3d(&role.out_map, tile + a * 16384 + quad * 4096, a * 64, h,
+                                          (int)t + quad * 32);
+                    ptx::bulk_commit();
+                    ptx::bulk_wait_read_all();
+                }
+            } else {   // a sequence ends in these rows: the ones behind it are not this sequence's
+                for (int x = lane; x < 32 * (DC / 8); x += 32) {
+                    const int r = quad * 32 + x / (DC / 8), cg = x % (DC / 8);
+                    if (r < len)
+                        *reinterpret_cast<uint4 *>(role.out + ((t + r) * g.H + h) * DC + cg * 8) =
+                            ptx::lds128(tile + (cg >> 3) * 16384 + swz(r, cg & 7));
+                }
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar_out + 8 * s);
             ++n;
         }
         if (!ok && lane == 0) flag_status(KDA_DEV_WAIT_TIMEOUT);
     } else {
-        // ---------------- state.  Thread <-> state row, and <-> token row when it weighs b; half the columns.
-        constexpr int CPT = DC / 2, BG = DAB / 16;   // state columns, 16-byte groups of a b row
-        const int quad = warp & 3, half = (warp - 6) >> 2, r = quad * 32 + lane, col = half * CPT;
+        // ---------------- state.  Thread <-> state row, and <-> token row when it weighs b; half of the columns.
+        constexpr int SP = kStateWarps / 4, CPT = DC / SP, BG = DAB / 8 / SP;   // state columns, 16-byte groups of a b row
+        const int quad = warp & 3, part = (warp - 6) >> 2, r = quad * 32 + lane, col = part * CPT;
         const uint32_t tl = ((uint32_t)(quad * 32) << 16) + col;
+        auto wait_state = [&](uint32_t bar, uint32_t parity) {
+            return wait_group<2, kStateWarps * 32>(warp == 6, bar, parity);
+        };
         const bool has = r < DAB;
         float S[CPT];
         int head = -1, wlen = -1, nu = 0;
-        float wt = 0.f;                          // this token row's weight
+        Weight wt(0.f);                          // this token row's
         float2 dec = make_float2(0.f, 0.f);      // decay of the chunk
         while (it.next(g)) {
             const uint32_t ph = (uint32_t)(n & 1);
@@ -606,14 +738,14 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
                 head = h;
                 wlen = len;
                 const float lg = log_decay[h];
-                wt = r < len ? (float)exp((double)lg * (dir > 0 ? len - 1 - r : r + 1)) : 0.f;
+                wt = Weight(r < len ? (float)exp((double)lg * (dir > 0 ? len - 1 - r : r + 1)) : 0.f);
                 dec = decay2(lg, len);
             }
             if (it.first) {
                 const float *src = nullptr;
                 const int row = state_row(slots, num_slots, it.cur.n);
                 if (it.from_before) src = y.start + (long long)w * DAB * DC;
-                else if (y.s0_copy && !it.whole_tail()) src = y.s0_copy + ((long long)it.cur.n * g.H + h) * (DAB * DC);
+                else if (y.s0_copy && !it.whole) src = y.s0_copy + ((long long)it.cur.n * g.H + h) * (DAB * DC);
                 else if (y.s0 && row >= 0) src = y.s0 + ((long long)row * g.H + h) * (DAB * DC);
                 if (!src || !has) {
 #pragma unroll
@@ -635,64 +767,77 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
 #pragma unroll
                 for (int k = 0; k < CPT / 8; ++k) {
                     const int cg = col / 8 + k;
-                    *reinterpret_cast<uint4 *>(sm + L::X + (cg >> 3) * (DAB * 128) + swz(r, cg & 7)) =
-                        make_uint4(pack2(S[8 * k], S[8 * k + 1]), pack2(S[8 * k + 2], S[8 * k + 3]),
-                                   pack2(S[8 * k + 4], S[8 * k + 5]), pack2(S[8 * k + 6], S[8 * k + 7]));
+                    ptx::sts128(sb + L::X + (cg >> 3) * (DAB * 128) + swz(r, cg & 7), pack2(S[8 * k], S[8 * k + 1]),
+                                pack2(S[8 * k + 2], S[8 * k + 3]), pack2(S[8 * k + 4], S[8 * k + 5]),
+                                pack2(S[8 * k + 6], S[8 * k + 7]));
                 }
             }
             ptx::fence_proxy_async_smem();
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar_x);
-            uint8_t *at = sm + L::ST0 + s * L::STAGE, *bt = at + L::AT, *ct = bt + L::AT;
-            if (!(ok = wait_warp(bar_full + 8 * s, (uint32_t)((n / NST) & 1)))) break;
+            const uint32_t at = sb + L::ST0 + s * L::STAGE, bt = at + L::AT, ct = bt + L::AT;
+            if (!(ok = wait_state(bar_full + 8 * s, (uint32_t)((n / NST) & 1)))) break;
             if (r >= len) {   // what lies behind the end may be another sequence's, or anything
 #pragma unroll
                 for (int k = 0; k < CPT / 8; ++k) {
                     const int cg = col / 8 + k;
-                    *reinterpret_cast<uint4 *>(ct + (cg >> 3) * 16384 + swz(r, cg & 7)) = make_uint4(0, 0, 0, 0);
+                    ptx::sts128(ct + (cg >> 3) * 16384 + swz(r, cg & 7), 0, 0, 0, 0);
                 }
             }
             // inter done: scores are taken too, the tiles of A and X are free
-            if (!(ok = wait_warp(bar_in, ph))) break;
-            const bool need = !it.part_over() || (it.ends && want_last);
+            if (!(ok = wait_state(bar_in, ph))) break;
+            const bool need = it.need_u(want_last);
             if (need) {
+                const bool three = want_last && it.whole;
+                // four groups a step: their loads in flight together, and a body that fits the instruction cache
+#pragma unroll 1
+                for (int k = 0; k < BG; k += 4) {
+                    uint4 x[4];
+                    uint32_t off[4];
 #pragma unroll
-                for (int k = 0; k < BG; ++k) {
-                    const int cg = half * BG + k;
-                    const uint32_t off = (cg >> 3) * 16384 + swz(r, cg & 7);
-                    uint4 t0 = make_uint4(0, 0, 0, 0), t1 = t0, t2 = t0;
-                    if (r < len) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(bt + off);
-                        if (want_last) split8<true>(x, wt, t0, t1, t2);
-                        else split8<false>(x, wt, t0, t1, t2);
+                    for (int z = 0; z < 4; ++z) {
+                        const int cg = part * BG + k + z;
+                        off[z] = (cg >> 3) * 16384 + swz(r, cg & 7);
+                        x[z] = ptx::lds128(bt + off[z]);
                     }
-                    *reinterpret_cast<uint4 *>(bt + off) = t0;
-                    *reinterpret_cast<uint4 *>(at + off) = t1;
-                    if (want_last) *reinterpret_cast<uint4 *>(sm + L::X + off) = t2;
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        uint4 t0, t1, t2;
+                        if (r >= len) x[z] = make_uint4(0, 0, 0, 0);
+                        if (three) split8<true>(x[z], wt, t0, t1, t2);
+                        else split8<false>(x[z], wt, t0, t1, t2);
+                        ptx::sts128(bt + off[z], t0);
+                        ptx::sts128(at + off[z], t1);
+                        if (three) ptx::sts128(sb + L::X + off[z], t2);
+                    }
                 }
             }
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar_b);
             if (need) {
-                if (!(ok = wait_warp(bar_u, (uint32_t)(nu & 1)))) break;
+                if (!(ok = wait_state(bar_u, (uint32_t)(nu & 1)))) break;
                 ++nu;
                 ptx::tc_fence_after();
                 if (quad * 32 < DAB) {
 #pragma unroll
-                    for (int b = 0; b < CPT / 16; ++b) {
-                        float v[16];
-                        ptx::tmem_ld16(t_u + tl + 16 * b, v);
+                    for (int b = 0; b < CPT / 32; ++b) {
+                        float v[32];
+                        ptx::tmem_ld32(t_u + tl + 32 * b, v);
                         ptx::tmem_wait_ld();
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) {
-                            float &z = S[16 * b + x];
-                            z = fmaf(dec.x, z, fmaf(dec.y, z, v[x]));
+                        for (int x = 0; x < 32; x += 2) {
+                            float *z = S + 32 * b + x;
+                            const float2 o = make_float2(z[0], z[1]);
+                            const float2 n2 = ptx::fma2(make_float2(dec.x, dec.x), o,
+                                                        ptx::fma2(make_float2(dec.y, dec.y), o, make_float2(v[x], v[x + 1])));
+                            z[0] = n2.x;
+                            z[1] = n2.y;
                         }
                     }
                 }
-                if (it.ends && want_last && has) {
+                if (it.ends && it.whole && want_last && has) {
                     const int row = state_row(slots, num_slots, it.cur.n);
                     if (row >= 0) {
                         float *dst = y.last + (((long long)row * g.H + h) * DAB + r) * DC + col;
@@ -722,9 +867,9 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
 namespace kda {
 namespace la {
 
-inline bool tile_map(CUtensorMap *m, const void *x, const Call &c, int d) {
+inline bool tile_map(CUtensorMap *m, const void *x, const Call &c, int d, int tokens = kBox) {
     return kda::tc::make_tmap(m, x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (long long)c.B * c.T, c.H, d, 64,
-                              CU_TENSOR_MAP_SWIZZLE_128B);
+                              CU_TENSOR_MAP_SWIZZLE_128B, tokens);
 }
 
 template <int DB, int DC>
@@ -751,8 +896,9 @@ template <int DK, int DV>
 cudaError_t tc_forward(const Call &c, const void *q, const void *k, const void *v, const float *s0, void *o,
                        float *last, float *ws) {
     const Geo g = geo_of<kC>(c);
-    CUtensorMap tq, tk, tv;
-    if (!tile_map(&tq, q, c, DK) || !tile_map(&tk, k, c, DK) || !tile_map(&tv, v, c, DV))
+    CUtensorMap tq, tk, tv, to;
+    if (!tile_map(&tq, q, c, DK) || !tile_map(&tk, k, c, DK) || !tile_map(&tv, v, c, DV) ||
+        !tile_map(&to, o, c, DV, kOutBox))
         return cudaErrorInvalidValue;
     Carry y = carry_at(ws, g.W, DK * DV);
     y.s0 = s0;
@@ -762,12 +908,12 @@ cudaError_t tc_forward(const Call &c, const void *q, const void *k, const void *
     cudaError_t e;
     if (cuts<kC>(g)) {
         SumArgs a{};
-        a.role[0] = SumRole{tk, tv, y.sum_in, y.sum_out, 1};
+        a.role[0] = SumRole{tk, tv, y.sum_in, y.sum_out, 1, last != nullptr};
         if ((e = launch_sum<DK, DV>(g, a, 1, c)) != cudaSuccess) return e;
-        if ((e = launch_join<kC, 1>(g, y, c, DK * DV)) != cudaSuccess) return e;
+        if ((e = launch_join<kC, 1, true>(g, y, c, DK * DV)) != cudaSuccess) return e;
     }
     WalkArgs a{};
-    a.role[0] = WalkRole{tq, tk, tv, (__nv_bfloat16 *)o, y, 1, 0};
+    a.role[0] = WalkRole{tq, tk, tv, to, (__nv_bfloat16 *)o, y, 1, 0};
     return launch_walk<DK, DV>(g, a, 1, c);
 }
 
@@ -776,8 +922,9 @@ cudaError_t tc_backward(const Call &c, const void *q, const void *k, const void 
                         const float *dlast, void *dq, void *dk, void *dv, float *dinit, float *ws) {
     const Geo g = geo_of<kC>(c);
     constexpr int E = DK * DV;
-    CUtensorMap tq, tk, tv, td;
-    if (!tile_map(&tq, q, c, DK) || !tile_map(&tk, k, c, DK) || !tile_map(&tv, v, c, DV) || !tile_map(&td, d_o, c, DV))
+    CUtensorMap tq, tk, tv, td, odq, odk, odv;
+    if (!tile_map(&tq, q, c, DK) || !tile_map(&tk, k, c, DK) || !tile_map(&tv, v, c, DV) || !tile_map(&td, d_o, c, DV) ||
+        !tile_map(&odq, dq, c, DK, kOutBox) || !tile_map(&odk, dk, c, DK, kOutBox) || !tile_map(&odv, dv, c, DV, kOutBox))
         return cudaErrorInvalidValue;
     Carry fwd = carry_at(ws, g.W, E), bwd = carry_at(ws + (size_t)3 * g.W * E, g.W, E);
     fwd.s0 = s0;
@@ -786,16 +933,16 @@ cudaError_t tc_backward(const Call &c, const void *q, const void *k, const void 
     cudaError_t e;
     if (cuts<kC>(g)) {
         SumArgs a{};
-        a.role[0] = SumRole{tk, tv, fwd.sum_in, fwd.sum_out, 1};
-        a.role[1] = SumRole{tq, td, bwd.sum_in, bwd.sum_out, -1};
+        a.role[0] = SumRole{tk, tv, fwd.sum_in, fwd.sum_out, 1, 0};
+        a.role[1] = SumRole{tq, td, bwd.sum_in, bwd.sum_out, -1, dinit != nullptr};
         if ((e = launch_sum<DK, DV>(g, a, 2, c)) != cudaSuccess) return e;
-        if ((e = launch_join<kC, 1>(g, fwd, c, E)) != cudaSuccess) return e;
-        if ((e = launch_join<kC, -1>(g, bwd, c, E)) != cudaSuccess) return e;
+        if ((e = launch_join<kC, 1, true>(g, fwd, c, E)) != cudaSuccess) return e;
+        if ((e = launch_join<kC, -1, true>(g, bwd, c, E)) != cudaSuccess) return e;
     }
     Carry bwd_t = bwd;
     bwd_t.last = nullptr;
-    const WalkRole r_dq{td, tv, tk, (__nv_bfloat16 *)dq, fwd, 1, 1}, r_dk{tv, td, tq, (__nv_bfloat16 *)dk, bwd_t, -1, 1},
-        r_dv{tk, tq, td, (__nv_bfloat16 *)dv, bwd, -1, 0};
+    const WalkRole r_dq{td, tv, tk, odq, (__nv_bfloat16 *)dq, fwd, 1, 1}, r_dk{tv, td, tq, odk, (__nv_bfloat16 *)dk, bwd_t, -1, 1},
+        r_dv{tk, tq, td, odv, (__nv_bfloat16 *)dv, bwd, -1, 0};
     WalkArgs a{};
     a.role[0] = r_dq;
     a.role[1] = r_dk;
