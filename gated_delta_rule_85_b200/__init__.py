@@ -19,6 +19,7 @@ shares its layouts, states and slots; group_norm is the norm behind either kind 
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from types import SimpleNamespace
 
@@ -564,13 +565,24 @@ def _expect(name, t, shape, dtype):
         raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
 
 
-def _call(dev, entry, *args):
-    """One library call on dev's current stream (the last argument)."""
-    if dev.index == torch.cuda.current_device():
-        rc = entry(*args, torch.cuda.current_stream(dev).cuda_stream)
+# A small call's time is the host's, so the wrappers below ask each question once, in one
+# expression; only a call that fails it goes through the refusals that name the tensor.
+
+def _placed(index, tensors):
+    """Every given tensor is a contiguous one on CUDA device `index`."""
+    for t in tensors:
+        if t is not None and (t.get_device() != index or not t.is_contiguous()):
+            return False
+    return index >= 0
+
+
+def _call(index, entry, *args):
+    """One library call on the current stream (the last argument) of CUDA device `index`."""
+    if index == torch.cuda.current_device():
+        rc = entry(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(dev):
-            rc = entry(*args, torch.cuda.current_stream(dev).cuda_stream)
+        with torch.cuda.device(index):
+            rc = entry(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc != 0:
         raise KDAError(rc, last_error())
 
@@ -583,15 +595,34 @@ def _scratch(workspace, need, dev):
     return workspace, workspace.numel() * workspace.element_size()
 
 
+# sizes alone decide these; asking the library costs as much as a launch
+@functools.lru_cache(maxsize=1024)
+def _la_need(B, T, H, dk, dv, N, dt, slots):
+    return int(load_library().kda_la_chunk_forward_workspace_size(B, T, H, dk, dv, N, dt, slots))
+
+
+@functools.lru_cache(maxsize=1024)
+def _la_backward_need(B, T, H, dk, dv, N, dt):
+    return int(load_library().kda_la_chunk_backward_workspace_size(B, T, H, dk, dv, N, dt))
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_need(N, L, C, G, dt, backward):
+    return int(load_library().kda_group_norm_workspace_size(N, L, C, G, dt, backward))
+
+
 def _la_shapes(q, k, v, log_decay, cu_seqlens):
-    if q.dim() != 4 or v.dim() != 4:
+    qs, vs = q.shape, v.shape
+    if len(qs) != 4 or len(vs) != 4:
         raise ValueError("q, k and v must be [B, T, H, d]")
-    B, T, H, dk = q.shape
-    dv = v.shape[3]
-    dt = _dtype_code(q)
-    _expect("k", k, q.shape, q.dtype)
-    _expect("v", v, (B, T, H, dv), q.dtype)
-    _expect("log_decay", log_decay, (H,), torch.float32)
+    B, T, H, dk = qs
+    dv = vs[3]
+    dt, dtype = _dtype_code(q), q.dtype
+    if k.shape != qs or vs != (B, T, H, dv) or log_decay.shape != (H,) or k.dtype != dtype or v.dtype != dtype \
+            or log_decay.dtype != torch.float32:
+        _expect("k", k, qs, dtype)
+        _expect("v", v, (B, T, H, dv), dtype)
+        _expect("log_decay", log_decay, (H,), torch.float32)
     if cu_seqlens is None:
         return B, T, H, dk, dv, B, dt
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or cu_seqlens.dtype != torch.int32:
@@ -602,13 +633,13 @@ def _la_shapes(q, k, v, log_decay, cu_seqlens):
 def la_workspace_size(B, T, H, dk, dv, num_seqs, dtype=torch.bfloat16, slots=False) -> int:
     """Workspace bytes of la_chunk_forward (slots=True: of la_chunk_forward_slots)."""
     code = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}[dtype]
-    return int(load_library().kda_la_chunk_forward_workspace_size(B, T, H, dk, dv, num_seqs, code, int(slots)))
+    return _la_need(B, T, H, dk, dv, num_seqs, code, int(slots))
 
 
 def la_backward_workspace_size(B, T, H, dk, dv, num_seqs, dtype=torch.bfloat16) -> int:
     """Workspace bytes of la_chunk_backward."""
     code = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}[dtype]
-    return int(load_library().kda_la_chunk_backward_workspace_size(B, T, H, dk, dv, num_seqs, code))
+    return _la_backward_need(B, T, H, dk, dv, num_seqs, code)
 
 
 def la_chunk_forward(q, k, v, log_decay, init_state=None, cu_seqlens=None, *, o=None, final_state=True,
@@ -622,23 +653,25 @@ def la_chunk_forward(q, k, v, log_decay, init_state=None, cu_seqlens=None, *, o=
     Returns (o, final_state or None).
     """
     B, T, H, dk, dv, N, dt = _la_shapes(q, k, v, log_decay, cu_seqlens)
-    dev = q.device
-    _expect("init_state", init_state, (N, H, dk, dv), torch.float32)
+    state = (N, H, dk, dv)
+    if init_state is not None:
+        _expect("init_state", init_state, state, torch.float32)
     if o is None:
         o = torch.empty_like(v)
     else:
         _expect("o", o, v.shape, q.dtype)
     if final_state is True:
-        final_state = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+        final_state = torch.empty(state, dtype=torch.float32, device=q.device)
     elif final_state is False:
         final_state = None
     else:
-        _expect("final_state", final_state, (N, H, dk, dv), torch.float32)
-    _on_device(dev, q=q, k=k, v=v, log_decay=log_decay, init_state=init_state, cu_seqlens=cu_seqlens, o=o,
-               final_state=final_state)
-    lib = load_library()
-    ws, nb = _scratch(workspace, lib.kda_la_chunk_forward_workspace_size(B, T, H, dk, dv, N, dt, 0), dev)
-    _call(dev, lib.kda_la_chunk_forward, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+        _expect("final_state", final_state, state, torch.float32)
+    index = q.get_device()
+    if not _placed(index, (q, k, v, log_decay, init_state, cu_seqlens, o, final_state)):
+        _on_device(q.device, q=q, k=k, v=v, log_decay=log_decay, init_state=init_state, cu_seqlens=cu_seqlens, o=o,
+                   final_state=final_state)
+    ws, nb = _scratch(workspace, _la_need(B, T, H, dk, dv, N, dt, 0), q.device)
+    _call(index, load_library().kda_la_chunk_forward, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
           _ptr(init_state), o.data_ptr(), _ptr(final_state), _ptr(cu_seqlens), B, T, H, dk, dv, N, dt, _ptr(ws), nb)
     return o, final_state
 
@@ -648,20 +681,20 @@ def la_chunk_forward_slots(q, k, v, log_decay, state_pool, slots, cu_seqlens=Non
     starts from state_pool[slots[n]] and its final state is written back there (slot -1:
     start from zeros, write nothing).  Returns o."""
     B, T, H, dk, dv, N, dt = _la_shapes(q, k, v, log_decay, cu_seqlens)
-    dev = q.device
     _expect("state_pool", state_pool, (*state_pool.shape[:1], H, dk, dv), torch.float32)
     _expect("slots", slots, (N,), torch.int32)
     if o is None:
         o = torch.empty_like(v)
     else:
         _expect("o", o, v.shape, q.dtype)
-    _on_device(dev, q=q, k=k, v=v, log_decay=log_decay, state_pool=state_pool, slots=slots, cu_seqlens=cu_seqlens,
-               o=o)
-    lib = load_library()
-    ws, nb = _scratch(workspace, lib.kda_la_chunk_forward_workspace_size(B, T, H, dk, dv, N, dt, 1), dev)
-    _call(dev, lib.kda_la_chunk_forward_slots, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-          state_pool.data_ptr(), slots.data_ptr(), o.data_ptr(), _ptr(cu_seqlens), B, T, H, dk, dv, N,
-          state_pool.shape[0], dt, _ptr(ws), nb)
+    index = q.get_device()
+    if not _placed(index, (q, k, v, log_decay, state_pool, slots, cu_seqlens, o)):
+        _on_device(q.device, q=q, k=k, v=v, log_decay=log_decay, state_pool=state_pool, slots=slots,
+                   cu_seqlens=cu_seqlens, o=o)
+    ws, nb = _scratch(workspace, _la_need(B, T, H, dk, dv, N, dt, 1), q.device)
+    _call(index, load_library().kda_la_chunk_forward_slots, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          log_decay.data_ptr(), state_pool.data_ptr(), slots.data_ptr(), o.data_ptr(), _ptr(cu_seqlens), B, T, H, dk,
+          dv, N, state_pool.shape[0], dt, _ptr(ws), nb)
     return o
 
 
@@ -692,40 +725,46 @@ def la_chunk_backward(q, k, v, log_decay, d_o, init_state=None, dfinal_state=Non
         g["dinit_state"] = torch.empty(state, dtype=torch.float32, device=dev)
     else:
         _expect("dinit_state", g["dinit_state"], state, torch.float32)
-    _on_device(dev, q=q, k=k, v=v, log_decay=log_decay, init_state=init_state, d_o=d_o, dfinal_state=dfinal_state,
-               cu_seqlens=cu_seqlens, **g)
-    lib = load_library()
-    ws, nb = _scratch(workspace, lib.kda_la_chunk_backward_workspace_size(B, T, H, dk, dv, N, dt), dev)
-    _call(dev, lib.kda_la_chunk_backward, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+    index = q.get_device()
+    if not _placed(index, (q, k, v, log_decay, init_state, d_o, dfinal_state, cu_seqlens, *g.values())):
+        _on_device(dev, q=q, k=k, v=v, log_decay=log_decay, init_state=init_state, d_o=d_o, dfinal_state=dfinal_state,
+                   cu_seqlens=cu_seqlens, **g)
+    ws, nb = _scratch(workspace, _la_backward_need(B, T, H, dk, dv, N, dt), dev)
+    _call(index, load_library().kda_la_chunk_backward, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
           _ptr(init_state), d_o.data_ptr(), _ptr(dfinal_state), g["dq"].data_ptr(), g["dk"].data_ptr(),
           g["dv"].data_ptr(), _ptr(g["dinit_state"]), _ptr(cu_seqlens), B, T, H, dk, dv, N, dt, _ptr(ws), nb)
     return g
 
 
-def _la_step_shapes(q, k, v, log_decay):
-    if q.dim() != 3 or v.dim() != 3:
+def _la_step_shapes(q, k, v, log_decay, name, state, rows, o):
+    """Sizes, and the output; `rows` is the number of states (None: any)."""
+    qs, vs, ss, dtype = q.shape, v.shape, state.shape, q.dtype
+    if len(qs) != 3 or len(vs) != 3:
         raise ValueError("q, k and v must be [N, H, d]")
-    N, H, dk = q.shape
-    dv = v.shape[2]
-    dt = _dtype_code(q)
-    _expect("k", k, q.shape, q.dtype)
-    _expect("v", v, (N, H, dv), q.dtype)
-    _expect("log_decay", log_decay, (H,), torch.float32)
-    return N, H, dk, dv, dt
+    N, H, dk = qs
+    dv = vs[2]
+    if o is None:
+        o = torch.empty_like(v)
+    if k.shape != qs or vs != (N, H, dv) or log_decay.shape != (H,) or ss[1:] != (H, dk, dv) or o.shape != vs \
+            or (rows is not None and ss[0] != N) or k.dtype != dtype or v.dtype != dtype or o.dtype != dtype \
+            or log_decay.dtype != torch.float32 or state.dtype != torch.float32:
+        _dtype_code(q)
+        _expect("k", k, qs, dtype)
+        _expect("v", v, (N, H, dv), dtype)
+        _expect("log_decay", log_decay, (H,), torch.float32)
+        _expect(name, state, (*(ss[:1] if rows is None else (N,)), H, dk, dv), torch.float32)
+        _expect("o", o, vs, dtype)
+    return N, H, dk, dv, _dtype_code(q), o
 
 
 def la_recurrent_step(q, k, v, log_decay, state, o=None):
     """One token of linear attention with a decay for each head (kda_la_recurrent_step);
     `state` [N, H, dk, dv] float32 is updated in place.  Returns o."""
-    N, H, dk, dv, dt = _la_step_shapes(q, k, v, log_decay)
-    dev = q.device
-    _expect("state", state, (N, H, dk, dv), torch.float32)
-    if o is None:
-        o = torch.empty_like(v)
-    else:
-        _expect("o", o, v.shape, q.dtype)
-    _on_device(dev, q=q, k=k, v=v, log_decay=log_decay, state=state, o=o)
-    _call(dev, load_library().kda_la_recurrent_step, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+    N, H, dk, dv, dt, o = _la_step_shapes(q, k, v, log_decay, "state", state, 0, o)
+    index = q.get_device()
+    if not _placed(index, (q, k, v, log_decay, state, o)):
+        _on_device(q.device, q=q, k=k, v=v, log_decay=log_decay, state=state, o=o)
+    _call(index, load_library().kda_la_recurrent_step, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
           state.data_ptr(), o.data_ptr(), N, H, dk, dv, dt)
     return o
 
@@ -733,16 +772,12 @@ def la_recurrent_step(q, k, v, log_decay, state, o=None):
 def la_recurrent_step_slots(q, k, v, log_decay, state_pool, slots, o=None):
     """la_recurrent_step on a state pool (kda_la_recurrent_step_slots): sequence n uses and
     updates state_pool[slots[n]] in place (slot -1: padding, o row zero).  Returns o."""
-    N, H, dk, dv, dt = _la_step_shapes(q, k, v, log_decay)
-    dev = q.device
-    _expect("state_pool", state_pool, (*state_pool.shape[:1], H, dk, dv), torch.float32)
+    N, H, dk, dv, dt, o = _la_step_shapes(q, k, v, log_decay, "state_pool", state_pool, None, o)
     _expect("slots", slots, (N,), torch.int32)
-    if o is None:
-        o = torch.empty_like(v)
-    else:
-        _expect("o", o, v.shape, q.dtype)
-    _on_device(dev, q=q, k=k, v=v, log_decay=log_decay, state_pool=state_pool, slots=slots, o=o)
-    _call(dev, load_library().kda_la_recurrent_step_slots, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    index = q.get_device()
+    if not _placed(index, (q, k, v, log_decay, state_pool, slots, o)):
+        _on_device(q.device, q=q, k=k, v=v, log_decay=log_decay, state_pool=state_pool, slots=slots, o=o)
+    _call(index, load_library().kda_la_recurrent_step_slots, q.data_ptr(), k.data_ptr(), v.data_ptr(),
           log_decay.data_ptr(), state_pool.data_ptr(), slots.data_ptr(), o.data_ptr(), N, H, dk, dv,
           state_pool.shape[0], dt)
     return o
@@ -752,28 +787,33 @@ ACTIVATIONS = {"none": 0, "silu": 1, "sigmoid": 2}   # KDA_ACT_*
 
 
 def _norm_shapes(x, num_groups, weight, bias, gate, activation):
-    if x.dim() < 2:
+    xs = x.shape
+    if len(xs) < 2:
         raise ValueError("x must be [N, ..., C], channels last")
-    if activation not in ACTIVATIONS:
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
-    N, C = x.shape[0], x.shape[-1]
+    N, C = xs[0], xs[-1]
     L = 1
-    for n in x.shape[1:-1]:
+    for n in xs[1:-1]:
         L *= n
     if num_groups < 1 or C % num_groups:
         raise ValueError(f"{C} channels do not divide into {num_groups} groups")
     if L < 1 or C < 1:
         raise ValueError("a sample must hold at least one position and one channel")
-    _expect("weight", weight, (C,), torch.float32)
-    _expect("bias", bias, (C,), torch.float32)
-    _expect("gate", gate, x.shape, x.dtype)
-    return N, L, C, _dtype_code(x), ACTIVATIONS[activation]
+    if weight is not None:
+        _expect("weight", weight, (C,), torch.float32)
+    if bias is not None:
+        _expect("bias", bias, (C,), torch.float32)
+    if gate is not None:
+        _expect("gate", gate, xs, x.dtype)
+    return N, L, C, _dtype_code(x), act
 
 
 def group_norm_workspace_size(N, L, C, num_groups, dtype=torch.bfloat16, backward=False) -> int:
     """Workspace bytes of group_norm (or of group_norm_backward) for x [N, L positions, C]."""
     code = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}[dtype]
-    return int(load_library().kda_group_norm_workspace_size(N, L, C, num_groups, code, int(backward)))
+    return _norm_need(N, L, C, num_groups, code, int(backward))
 
 
 def group_norm(x, num_groups, weight=None, bias=None, gate=None, *, eps=1e-5, activation="silu", y=None,
@@ -789,18 +829,18 @@ def group_norm(x, num_groups, weight=None, bias=None, gate=None, *, eps=1e-5, ac
     N, L, C, dt, act = _norm_shapes(x, num_groups, weight, bias, gate, activation)
     if not eps > 0:
         raise ValueError(f"eps must be above 0, got {eps}")
-    dev = x.device
     if y is None:
         y = torch.empty_like(x)
     else:
         _expect("y", y, x.shape, x.dtype)
-    _on_device(dev, x=x, weight=weight, bias=bias, gate=gate, y=y)
-    mean = torch.empty((N, num_groups), dtype=torch.float32, device=dev)
-    rstd = torch.empty((N, num_groups), dtype=torch.float32, device=dev)
-    lib = load_library()
-    ws, nb = _scratch(workspace, lib.kda_group_norm_workspace_size(N, L, C, num_groups, dt, 0), dev)
-    _call(dev, lib.kda_group_norm_forward, x.data_ptr(), _ptr(weight), _ptr(bias), _ptr(gate), y.data_ptr(),
-          mean.data_ptr(), rstd.data_ptr(), N, L, C, num_groups, eps, act, dt, _ptr(ws), nb)
+    index = x.get_device()
+    if not _placed(index, (x, weight, bias, gate, y)):
+        _on_device(x.device, x=x, weight=weight, bias=bias, gate=gate, y=y)
+    dev = x.device
+    mean, rstd = torch.empty((2, N, num_groups), dtype=torch.float32, device=dev).unbind()
+    ws, nb = _scratch(workspace, _norm_need(N, L, C, num_groups, dt, 0), dev)
+    _call(index, load_library().kda_group_norm_forward, x.data_ptr(), _ptr(weight), _ptr(bias), _ptr(gate),
+          y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), N, L, C, num_groups, eps, act, dt, _ptr(ws), nb)
     return y, mean, rstd
 
 
@@ -822,12 +862,13 @@ def group_norm_backward(dy, x, mean, rstd, num_groups, weight=None, bias=None, g
             g[name] = torch.empty_like(like)
         else:
             _expect(name, g[name], like.shape, like.dtype)
-    _on_device(dev, dy=dy, x=x, mean=mean, rstd=rstd, weight=weight, bias=bias, gate=gate, **g)
-    lib = load_library()
-    ws, nb = _scratch(workspace, lib.kda_group_norm_workspace_size(N, L, C, num_groups, dt, 1), dev)
-    _call(dev, lib.kda_group_norm_backward, dy.data_ptr(), x.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
-          _ptr(weight), _ptr(bias), _ptr(gate), g["dx"].data_ptr(), _ptr(g.get("dgate")), _ptr(g.get("dweight")),
-          _ptr(g.get("dbias")), N, L, C, num_groups, act, dt, _ptr(ws), nb)
+    index = x.get_device()
+    if not _placed(index, (dy, x, mean, rstd, weight, bias, gate, *g.values())):
+        _on_device(dev, dy=dy, x=x, mean=mean, rstd=rstd, weight=weight, bias=bias, gate=gate, **g)
+    ws, nb = _scratch(workspace, _norm_need(N, L, C, num_groups, dt, 1), dev)
+    _call(index, load_library().kda_group_norm_backward, dy.data_ptr(), x.data_ptr(), mean.data_ptr(),
+          rstd.data_ptr(), _ptr(weight), _ptr(bias), _ptr(gate), g["dx"].data_ptr(), _ptr(g.get("dgate")),
+          _ptr(g.get("dweight")), _ptr(g.get("dbias")), N, L, C, num_groups, act, dt, _ptr(ws), nb)
     return g
 
 

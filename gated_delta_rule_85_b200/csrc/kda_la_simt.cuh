@@ -278,9 +278,11 @@ Geo geo_of(const Call &c) {
     return g;
 }
 
-// Does a span boundary fall inside a sequence?  Packed lengths are on the device: assume so.
+// Does a span boundary fall inside a sequence?  Packed lengths are on the device: any of
+// more than one chunk may be cut.
 template <int C>
 bool cuts(const Geo &g) {
+    if (g.T <= C) return false;
     if (g.cu) return true;
     const int per = (g.T + C - 1) / C;
     for (int w = 1; w < g.W; ++w)
@@ -303,6 +305,15 @@ cudaError_t launch_join(const Geo &g, const Carry &y, const Call &c, int E) {
     const dim3 grid(g.W + (g.cu ? g.N : 0), E / 1024);
     la_join_kernel<C, DIR, WANT_LAST><<<grid, 256, 0, c.st>>>(g, y, c.log_decay, E, c.slots, c.num_slots);
     return cudaGetLastError();
+}
+
+// Where nothing is cut the join has only empty packed sequences' states to hand through.
+template <int C>
+cudaError_t launch_empty(const Geo &g, const Carry &y, const Call &c, int E) {
+    if (!g.cu || !y.last || y.last == y.s0) return cudaSuccess;
+    Geo none = g;
+    none.W = 0;
+    return launch_join<C, 1, false>(none, y, c, E);
 }
 
 template <int DAB, int DC, typename Tin, int DIR, bool WALK>
@@ -329,6 +340,8 @@ cudaError_t simt_forward(const Call &c, const void *q, const void *k, const void
     if (cuts<kSimtC>(g)) {
         if ((e = launch_simt<DK, DV, Tin, 1, false>(g, wk, c)) != cudaSuccess) return e;
         if ((e = launch_join<kSimtC, 1, false>(g, wk.y, c, DK * DV)) != cudaSuccess) return e;
+    } else if ((e = launch_empty<kSimtC>(g, wk.y, c, DK * DV)) != cudaSuccess) {
+        return e;
     }
     return launch_simt<DK, DV, Tin, 1, true>(g, wk, c);
 }
@@ -350,6 +363,8 @@ cudaError_t simt_backward(const Call &c, const void *q, const void *k, const voi
         if ((e = launch_simt<DK, DV, Tin, -1, false>(g, sum_b, c)) != cudaSuccess) return e;
         if ((e = launch_join<kSimtC, 1, false>(g, fwd, c, E)) != cudaSuccess) return e;
         if ((e = launch_join<kSimtC, -1, false>(g, bwd, c, E)) != cudaSuccess) return e;
+    } else if ((e = launch_empty<kSimtC>(g, bwd, c, E)) != cudaSuccess) {
+        return e;
     }
     Carry bwd_t = bwd;
     bwd_t.last = nullptr;

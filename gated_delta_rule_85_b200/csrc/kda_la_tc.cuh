@@ -911,6 +911,8 @@ cudaError_t tc_forward(const Call &c, const void *q, const void *k, const void *
         a.role[0] = SumRole{tk, tv, y.sum_in, y.sum_out, 1, last != nullptr};
         if ((e = launch_sum<DK, DV>(g, a, 1, c)) != cudaSuccess) return e;
         if ((e = launch_join<kC, 1, true>(g, y, c, DK * DV)) != cudaSuccess) return e;
+    } else if ((e = launch_empty<kC>(g, y, c, DK * DV)) != cudaSuccess) {
+        return e;
     }
     WalkArgs a{};
     a.role[0] = WalkRole{tq, tk, tv, to, (__nv_bfloat16 *)o, y, 1, 0};
@@ -938,6 +940,8 @@ cudaError_t tc_backward(const Call &c, const void *q, const void *k, const void 
         if ((e = launch_sum<DK, DV>(g, a, 2, c)) != cudaSuccess) return e;
         if ((e = launch_join<kC, 1, true>(g, fwd, c, E)) != cudaSuccess) return e;
         if ((e = launch_join<kC, -1, true>(g, bwd, c, E)) != cudaSuccess) return e;
+    } else if ((e = launch_empty<kC>(g, bwd, c, E)) != cudaSuccess) {
+        return e;
     }
     Carry bwd_t = bwd;
     bwd_t.last = nullptr;

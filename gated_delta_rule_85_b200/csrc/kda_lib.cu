@@ -508,7 +508,9 @@ bool la_sizes_ok(int B, int T, int H, int dk, int dv, int num_seqs, int dtype) {
            (dtype == KDA_BF16 || dtype == KDA_F32);
 }
 
-size_t la_forward_ws(int H, int dk, int dv, int num_seqs, bool with_slots) {
+// A sequence of one chunk at most is never cut between CTAs and needs no carried state.
+size_t la_forward_ws(int T, int H, int dk, int dv, int num_seqs, int dtype, bool with_slots) {
+    if (T <= (dtype == KDA_BF16 ? kda::la::kC : kda::la::kSimtC)) return 0;
     return kda::la::carry_bytes(kda::la::kSMs, dk, dv) +
            (with_slots ? (size_t)num_seqs * H * dk * dv * sizeof(float) : 0);
 }
@@ -842,7 +844,7 @@ int kda_gdn_chunk_backward(const void *q, const void *k, const void *v, const fl
 size_t kda_la_chunk_forward_workspace_size(int B, int T, int H, int dk, int dv, int num_seqs, int dtype,
                                            int with_slots) {
     if (!la_sizes_ok(B, T, H, dk, dv, num_seqs, dtype) || T == 0 || num_seqs == 0) return 0;
-    return la_forward_ws(H, dk, dv, num_seqs, with_slots != 0);
+    return la_forward_ws(T, H, dk, dv, num_seqs, dtype, with_slots != 0);
 }
 
 int kda_la_chunk_forward(const void *q, const void *k, const void *v, const float *log_decay,
@@ -901,7 +903,7 @@ int kda_la_recurrent_step_slots(const void *q, const void *k, const void *v, con
 
 size_t kda_la_chunk_backward_workspace_size(int B, int T, int H, int dk, int dv, int num_seqs, int dtype) {
     if (!la_sizes_ok(B, T, H, dk, dv, num_seqs, dtype) || T == 0 || num_seqs == 0) return 0;
-    return 2 * la_forward_ws(H, dk, dv, num_seqs, false);
+    return 2 * la_forward_ws(T, H, dk, dv, num_seqs, dtype, false);
 }
 
 int kda_la_chunk_backward(const void *q, const void *k, const void *v, const float *log_decay,

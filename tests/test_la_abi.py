@@ -18,7 +18,7 @@ def lib():
 
 
 def prefill(lib, **over):
-    a = dict(q=A[0], k=A[1], v=A[2], g=A[3], s0=A[4], o=A[5], fs=A[6], cu=None, B=1, T=128, H=2, dk=128, dv=128, N=1,
+    a = dict(q=A[0], k=A[1], v=A[2], g=A[3], s0=A[4], o=A[5], fs=A[6], cu=None, B=1, T=256, H=2, dk=128, dv=128, N=1,
              dtype=0, ws=A[7], wsb=WS)
     a.update(over)
     return lib.kda_la_chunk_forward(*(a[x] for x in ("q", "k", "v", "g", "s0", "o", "fs", "cu", "B", "T", "H", "dk",
@@ -43,7 +43,7 @@ def test_prefill_rejects(lib, over, code):
 
 
 def slots(lib, **over):
-    a = dict(q=A[0], k=A[1], v=A[2], g=A[3], pool=A[4], slots=A[5], o=A[6], cu=None, B=1, T=128, H=2, dk=128, dv=128,
+    a = dict(q=A[0], k=A[1], v=A[2], g=A[3], pool=A[4], slots=A[5], o=A[6], cu=None, B=1, T=256, H=2, dk=128, dv=128,
              N=1, ns=4, dtype=0, ws=A[7], wsb=WS)
     a.update(over)
     return lib.kda_la_chunk_forward_slots(*(a[x] for x in ("q", "k", "v", "g", "pool", "slots", "o", "cu", "B", "T",
@@ -59,14 +59,16 @@ def test_slots_rejects(lib, over, code):
 
 def test_slots_workspace_holds_the_states(lib):
     f = lib.kda_la_chunk_forward_workspace_size
-    assert f(4, 100, 8, 64, 128, 4, 0, 1) == f(4, 100, 8, 64, 128, 4, 0, 0) + 4 * 8 * 64 * 128 * 4
+    assert f(4, 300, 8, 64, 128, 4, 0, 1) == f(4, 300, 8, 64, 128, 4, 0, 0) + 4 * 8 * 64 * 128 * 4
+    # one chunk a sequence: nothing is carried from CTA to CTA
+    assert f(4, 128, 8, 64, 128, 4, 0, 1) == 0 and f(4, 64, 8, 64, 128, 4, 1, 1) == 0 < f(4, 65, 8, 64, 128, 4, 1, 0)
     assert f(1, 1 << 20, 32, 128, 128, 1, 0, 0) == f(1, 256, 32, 128, 128, 1, 0, 0)   # not a function of T
     assert f(1, 0, 8, 64, 64, 1, 0, 0) == 0 and f(1, 64, 8, 96, 64, 1, 0, 0) == 0
 
 
 def backward(lib, **over):
     a = dict(q=A[0], k=A[1], v=A[2], g=A[3], s0=A[4], do=A[5], ds=A[6], dq=A[7], dkk=A[8], dvv=A[9], di=A[10], cu=None,
-             B=1, T=128, H=2, dk=128, dv=128, N=1, dtype=0, ws=A[11], wsb=WS)
+             B=1, T=256, H=2, dk=128, dv=128, N=1, dtype=0, ws=A[11], wsb=WS)
     a.update(over)
     return lib.kda_la_chunk_backward(*(a[x] for x in ("q", "k", "v", "g", "s0", "do", "ds", "dq", "dkk", "dvv", "di",
                                                       "cu", "B", "T", "H", "dk", "dv", "N", "dtype", "ws", "wsb")), None)
