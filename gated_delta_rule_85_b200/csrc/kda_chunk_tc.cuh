@@ -36,6 +36,7 @@
 
 #include "kda_common.cuh"
 #include "tc_ptx.cuh"
+#include "tc_tile.cuh"
 
 namespace kda {
 namespace tc {
@@ -155,18 +156,6 @@ __device__ __forceinline__ float4 ld_bf16x4(const uint8_t *p) {
 __device__ __forceinline__ void st_bf16x8(uint8_t *base, uint32_t off, const float *x) {
     *reinterpret_cast<uint4 *>(base + off) =
         make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-}
-
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// Descriptor of the 16-wide K step `s` of a K-major swizzled tile at `addr` with
-// `rows` rows per K atom, starting at row r0 (a multiple of 8).
-__device__ __forceinline__ uint64_t kdesc(uint32_t addr, int s, int rows, int r0 = 0) {
-    return ptx::desc_kmajor_sw128(addr + (uint32_t)((s >> 2) * rows * 128 + r0 * 128 + (s & 3) * 32));
 }
 
 __device__ __forceinline__ uint32_t f2tf32(float x) {
@@ -1004,37 +993,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 }
 
 // ------------------------------------------------------------------ host side
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                    const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-inline EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    if (!fn) {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    }
-    return fn;
-}
-
-// [tokens, H, inner] row-major tensor -> box (box_inner, 1, box_tokens).
-inline bool make_tmap(CUtensorMap *m, const void *base, CUtensorMapDataType dt, int esize, long long tokens,
-                      int H, int inner, int box_inner,
-                      CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE, int box_tokens = C) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)H, (cuuint64_t)tokens};
-    cuuint64_t strides[2] = {(cuuint64_t)inner * esize, (cuuint64_t)inner * esize * H};
-    cuuint32_t box[3] = {(cuuint32_t)box_inner, 1u, (cuuint32_t)box_tokens};
-    cuuint32_t estr[3] = {1u, 1u, 1u};
-    return fn(m, dt, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 template <int DK, int DVT, bool GS>
 int launch_t(const void *q, const void *k, const void *v, const float *log_alpha, const float *beta,

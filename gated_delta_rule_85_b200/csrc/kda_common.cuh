@@ -1,4 +1,4 @@
-// Shared device helpers for the KDA kernels (one translation unit: kda_lib.cu).
+// Shared device helpers for the kernels of every translation unit.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -9,8 +9,9 @@
 
 namespace kda {
 
-// Per-device status word; kernels OR KDA_DEV_* flags into it.
-__device__ unsigned int g_status;
+// Per-device status word of this translation unit; kernels OR KDA_DEV_* flags into it.  A unit
+// announces its word with KDA_STATUS_WORD (kda_host.h), and kda_get_device_status reads all.
+static __device__ unsigned int g_status;
 
 __device__ __forceinline__ void flag_status(unsigned int bits) { atomicOr(&g_status, bits); }
 

@@ -17,9 +17,9 @@
 // the states of cut ones are made by the first pass and the join.
 #pragma once
 
-#include "kda_chunk_tc.cuh"
 #include "kda_la.cuh"
 #include "tc_ptx.cuh"
+#include "tc_tile.cuh"
 
 namespace kda {
 namespace la {

@@ -1,5 +1,5 @@
-// libkda: the C ABI declared in include/kda.h.  One translation unit holds every
-// kernel so the device status word is a single symbol per device.
+// libkda: the C ABI declared in include/kda.h.  This unit holds the delta-rule entry points
+// and the host helpers of all units (kda_host.h).
 #include <algorithm>
 #include <atomic>
 #include <cstdarg>
@@ -14,15 +14,17 @@
 #include "kda_chunk_2pass.cuh"
 #include "kda_bwd_simt.cuh"
 #include "kda_bwd_tc.cuh"
-#include "kda_la.cuh"
-#include "kda_la_simt.cuh"
-#include "kda_la_tc.cuh"
-#include "kda_la_step.cuh"
-#include "kda_norm.cuh"
+#include "kda_host.h"
 
-namespace {
+KDA_STATUS_WORD;
 
-thread_local char g_err[512] = "";
+namespace kda {
+namespace host {
+
+static thread_local char g_err[512] = "";
+static StatusWord *g_words = nullptr;
+
+StatusWord::StatusWord(const void *s) : symbol(s), next(g_words) { g_words = this; }
 
 int fail(int code, const char *fmt, ...) {
     va_list ap;
@@ -32,8 +34,6 @@ int fail(int code, const char *fmt, ...) {
     return code;
 }
 
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 int cuda_fail(cudaError_t e, const char *what) {
     return fail(KDA_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
 }
@@ -42,7 +42,7 @@ int cuda_fail(cudaError_t e, const char *what) {
 int check_prefill(const void *q, const void *k, const void *v, const float *log_alpha,
                   const float *beta, const float *init_state, const void *o, const float *final_state,
                   const int32_t *cu_seqlens, int B, int T, int H, int dk, int dv, int num_seqs,
-                  int dtype, int chunk, bool gate_scalar = false) {
+                  int dtype, int chunk, bool gate_scalar) {
     if (B < 1 || T < 0 || H < 1 || num_seqs < 0)
         return fail(KDA_ERR_INVALID_ARG, "bad sizes B=%d T=%d H=%d num_seqs=%d", B, T, H, num_seqs);
     // With no tokens the per-token tensors are empty and may be NULL.
@@ -70,6 +70,48 @@ int check_prefill(const void *q, const void *k, const void *v, const float *log_
     if (cu_seqlens && !aligned(cu_seqlens, 4)) return fail(KDA_ERR_MISALIGNED, "cu_seqlens is not 4-byte aligned");
     return KDA_OK;
 }
+
+int check_decode(const void *q, const void *k, const void *v, const float *log_alpha, const float *beta,
+                 const float *state, const void *o, int N, int H, int dk, int dv, int dtype,
+                 bool gate_scalar) {
+    if (N < 0 || H < 1) return fail(KDA_ERR_INVALID_ARG, "bad sizes N=%d H=%d", N, H);
+    if (N == 0) return KDA_OK;   // nothing to do; empty tensors may carry NULL pointers
+    if (!q || !k || !v || !log_alpha || !beta || !state || !o)
+        return fail(KDA_ERR_INVALID_ARG, "q, k, v, log_alpha, beta, state and o are required");
+    if ((dk != 64 && dk != 128) || (dv != 64 && dv != 128))
+        return fail(KDA_ERR_UNSUPPORTED, "dk=%d dv=%d: each must be 64 or 128", dk, dv);
+    if (dtype != KDA_BF16 && dtype != KDA_F32) return fail(KDA_ERR_UNSUPPORTED, "dtype=%d", dtype);
+    const void *p16[] = {q, k, v, log_alpha, o, state};
+    const char *n16[] = {"q", "k", "v", "log_alpha", "o", "state"};
+    for (int i = 0; i < 6; ++i)
+        if (!aligned(p16[i], (i == 3 && gate_scalar) ? 4 : 16))
+            return fail(KDA_ERR_MISALIGNED, "%s is not %d-byte aligned", n16[i], (i == 3 && gate_scalar) ? 4 : 16);
+    if (!aligned(beta, 4)) return fail(KDA_ERR_MISALIGNED, "beta is not 4-byte aligned");
+    if ((long long)N * H > 0x7fffffffLL) return fail(KDA_ERR_UNSUPPORTED, "N*H=%lld too large", (long long)N * H);
+    return KDA_OK;
+}
+
+int check_workspace(const void *workspace, size_t ws_bytes, size_t need) {
+    if (need && (!workspace || ws_bytes < need))
+        return fail(KDA_ERR_WORKSPACE, "workspace of %zu bytes required, got %zu%s", need, ws_bytes,
+                    workspace ? "" : " (NULL)");
+    if (workspace && !aligned(workspace, 256)) return fail(KDA_ERR_MISALIGNED, "workspace is not 256-byte aligned");
+    return KDA_OK;
+}
+
+int state_passthrough(const float *init_state, float *final_state, int num_seqs, int H, int dk, int dv,
+                      cudaStream_t st) {
+    char msg[256] = "";
+    const int rc = kda::tc::state_passthrough(init_state, final_state, num_seqs, H, dk, dv, st, msg, sizeof(msg));
+    return rc ? fail(rc, "%s", msg) : KDA_OK;
+}
+
+}  // namespace host
+}  // namespace kda
+
+using namespace kda::host;
+
+namespace {
 
 // Which tensor-core schedule runs, the workspace it needs, and (two-pass on one
 // sequence longer than the budget allows) the window of tokens per launch pair.
@@ -311,26 +353,6 @@ int prefill_impl(const void *q, const void *k, const void *v, const float *log_a
 }
 
 // Decode argument checks shared by both decode entry points.
-int check_decode(const void *q, const void *k, const void *v, const float *log_alpha, const float *beta,
-                 const float *state, const void *o, int N, int H, int dk, int dv, int dtype,
-                 bool gate_scalar = false) {
-    if (N < 0 || H < 1) return fail(KDA_ERR_INVALID_ARG, "bad sizes N=%d H=%d", N, H);
-    if (N == 0) return KDA_OK;   // nothing to do; empty tensors may carry NULL pointers
-    if (!q || !k || !v || !log_alpha || !beta || !state || !o)
-        return fail(KDA_ERR_INVALID_ARG, "q, k, v, log_alpha, beta, state and o are required");
-    if ((dk != 64 && dk != 128) || (dv != 64 && dv != 128))
-        return fail(KDA_ERR_UNSUPPORTED, "dk=%d dv=%d: each must be 64 or 128", dk, dv);
-    if (dtype != KDA_BF16 && dtype != KDA_F32) return fail(KDA_ERR_UNSUPPORTED, "dtype=%d", dtype);
-    const void *p16[] = {q, k, v, log_alpha, o, state};
-    const char *n16[] = {"q", "k", "v", "log_alpha", "o", "state"};
-    for (int i = 0; i < 6; ++i)
-        if (!aligned(p16[i], (i == 3 && gate_scalar) ? 4 : 16))
-            return fail(KDA_ERR_MISALIGNED, "%s is not %d-byte aligned", n16[i], (i == 3 && gate_scalar) ? 4 : 16);
-    if (!aligned(beta, 4)) return fail(KDA_ERR_MISALIGNED, "beta is not 4-byte aligned");
-    if ((long long)N * H > 0x7fffffffLL) return fail(KDA_ERR_UNSUPPORTED, "N*H=%lld too large", (long long)N * H);
-    return KDA_OK;
-}
-
 int decode_impl(const void *q, const void *k, const void *v, const float *log_alpha, const float *beta,
                 float *state, void *o, int N, int H, int dk, int dv, int dtype, const int32_t *slots,
                 int num_slots, bool gate_scalar, cudaStream_t st, bool prologue = false) {
@@ -481,101 +503,6 @@ int backward_impl(const void *q, const void *k, const void *v, const float *log_
 #undef KDA_BWD_ARGS
 }
 
-// ------------------------------------------------------------------ linear attention with a decay for each head
-
-// Shared checks of the prefill and its backward pass; `states` names two optional fp32 state tensors.
-int check_la(const void *q, const void *k, const void *v, const float *log_decay, const float *s0, const void *o,
-             const float *last, const int32_t *cu_seqlens, int B, int T, int H, int dk, int dv, int num_seqs, int dtype) {
-    // beta is not part of this operator: log_decay stands in (both are 4-byte aligned device arrays)
-    int rc = check_prefill(q, k, v, log_decay, log_decay, s0, o, last, cu_seqlens, B, T, H, dk, dv, num_seqs, dtype, 64,
-                           true);
-    if (rc) return rc;
-    if ((long long)B * T > 0x7fffffffLL)
-        return fail(KDA_ERR_UNSUPPORTED, "B*T=%lld exceeds 2^31 - 1 tokens", (long long)B * T);
-    return KDA_OK;
-}
-
-int check_workspace(const void *workspace, size_t ws_bytes, size_t need) {
-    if (need && (!workspace || ws_bytes < need))
-        return fail(KDA_ERR_WORKSPACE, "workspace of %zu bytes required, got %zu%s", need, ws_bytes,
-                    workspace ? "" : " (NULL)");
-    if (workspace && !aligned(workspace, 256)) return fail(KDA_ERR_MISALIGNED, "workspace is not 256-byte aligned");
-    return KDA_OK;
-}
-
-bool la_sizes_ok(int B, int T, int H, int dk, int dv, int num_seqs, int dtype) {
-    return B >= 1 && T >= 0 && H >= 1 && num_seqs >= 0 && (dk == 64 || dk == 128) && (dv == 64 || dv == 128) &&
-           (dtype == KDA_BF16 || dtype == KDA_F32);
-}
-
-// A sequence of one chunk at most is never cut between CTAs and needs no carried state.
-size_t la_forward_ws(int T, int H, int dk, int dv, int num_seqs, int dtype, bool with_slots) {
-    if (T <= (dtype == KDA_BF16 ? kda::la::kC : kda::la::kSimtC)) return 0;
-    return kda::la::carry_bytes(kda::la::kSMs, dk, dv) +
-           (with_slots ? (size_t)num_seqs * H * dk * dv * sizeof(float) : 0);
-}
-
-int la_forward(const kda::la::Call &c, const void *q, const void *k, const void *v, const float *s0, void *o,
-               float *last, int dk, int dv, int dtype, void *ws) {
-    cudaError_t e = cudaErrorInvalidValue;
-#define KDA_LA(DK, DV)                                                                                          \
-    if (dk == DK && dv == DV)                                                                                   \
-        e = dtype == KDA_BF16                                                                                   \
-                ? kda::la::tc_forward<DK, DV>(c, q, k, v, s0, o, last, (float *)ws)                              \
-                : kda::la::simt_forward<DK, DV, float>(c, q, k, v, s0, o, last, (float *)ws)
-    KDA_LA(64, 64);
-    KDA_LA(64, 128);
-    KDA_LA(128, 64);
-    KDA_LA(128, 128);
-#undef KDA_LA
-    return e == cudaSuccess ? KDA_OK : cuda_fail(e, "linear attention launch");
-}
-
-int la_step(const void *q, const void *k, const void *v, const float *log_decay, float *state, void *o, int N, int H,
-            int dk, int dv, int dtype, const int32_t *slots, int num_slots, cudaStream_t st) {
-    const unsigned pairs = (unsigned)((long long)N * H);
-#define KDA_LA(DK, DV, TT)                                                                                       \
-    kda::la::la_step_kernel<DK, DV, TT><<<pairs, 256, 0, st>>>((const TT *)q, (const TT *)k, (const TT *)v, log_decay, \
-                                                               state, (TT *)o, slots, num_slots, H)
-#define KDA_LA2(DK, DV)                                                 \
-    if (dk == DK && dv == DV) {                                         \
-        if (dtype == KDA_BF16) KDA_LA(DK, DV, __nv_bfloat16);           \
-        else KDA_LA(DK, DV, float);                                     \
-    }
-    KDA_LA2(64, 64)
-    KDA_LA2(64, 128)
-    KDA_LA2(128, 64)
-    KDA_LA2(128, 128)
-#undef KDA_LA2
-#undef KDA_LA
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? KDA_OK : cuda_fail(e, "la_step launch");
-}
-
-// ------------------------------------------------------------------ group norm
-
-int check_norm(const void *x, const void *y, const float *mean, const float *rstd, const float *weight,
-               const float *bias, const void *gate, long long N, int L, int C, int G, int act, int dtype) {
-    if (N < 0 || L < 1 || C < 1 || G < 1) return fail(KDA_ERR_INVALID_ARG, "bad sizes N=%lld L=%d C=%d G=%d", N, L, C, G);
-    if (C % G) return fail(KDA_ERR_INVALID_ARG, "C=%d is not a multiple of G=%d", C, G);
-    if (act != KDA_ACT_NONE && act != KDA_ACT_SILU && act != KDA_ACT_SIGMOID)
-        return fail(KDA_ERR_INVALID_ARG, "act=%d is not a KDA_ACT_* value", act);
-    if (dtype != KDA_BF16 && dtype != KDA_F32) return fail(KDA_ERR_UNSUPPORTED, "dtype=%d", dtype);
-    if (C > (1 << 24) || L > (1 << 30)) return fail(KDA_ERR_UNSUPPORTED, "C=%d above 2^24 or L=%d above 2^30", C, L);
-    if (N > (1LL << 31) / G / 2 || N > 1LL << 24)
-        return fail(KDA_ERR_UNSUPPORTED, "N=%lld with G=%d: at most 2^24 samples and 2^30 groups", N, G);
-    if (N == 0) return KDA_OK;
-    if (!x || !y || !mean || !rstd) return fail(KDA_ERR_INVALID_ARG, "x, mean, rstd and the outputs are required");
-    const void *p16[] = {x, y, gate};
-    const char *n16[] = {"x", "y (dx)", "gate"};
-    for (int i = 0; i < 3; ++i)
-        if (p16[i] && !aligned(p16[i], 16)) return fail(KDA_ERR_MISALIGNED, "%s is not 16-byte aligned", n16[i]);
-    const void *p4[] = {mean, rstd, weight, bias};
-    for (int i = 0; i < 4; ++i)
-        if (p4[i] && !aligned(p4[i], 4)) return fail(KDA_ERR_MISALIGNED, "an fp32 array is not 4-byte aligned");
-    return KDA_OK;
-}
-
 }  // namespace
 
 namespace kda {
@@ -598,7 +525,7 @@ extern "C" {
 
 int kda_api_version(void) { return KDA_API_VERSION; }
 
-const char *kda_last_error(void) { return g_err; }
+const char *kda_last_error(void) { return kda::host::g_err; }
 
 size_t kda_chunk_forward_workspace_size_ex(int B, int T, int H, int dk, int dv, int num_seqs, int dtype,
                                            int chunk, int algo) {
@@ -841,163 +768,6 @@ int kda_gdn_chunk_backward(const void *q, const void *k, const void *v, const fl
                          stream, true);
 }
 
-size_t kda_la_chunk_forward_workspace_size(int B, int T, int H, int dk, int dv, int num_seqs, int dtype,
-                                           int with_slots) {
-    if (!la_sizes_ok(B, T, H, dk, dv, num_seqs, dtype) || T == 0 || num_seqs == 0) return 0;
-    return la_forward_ws(T, H, dk, dv, num_seqs, dtype, with_slots != 0);
-}
-
-int kda_la_chunk_forward(const void *q, const void *k, const void *v, const float *log_decay,
-                         const float *init_state, void *o, float *final_state, const int32_t *cu_seqlens, int B,
-                         int T, int H, int dk, int dv, int num_seqs, int dtype, void *workspace, size_t ws_bytes,
-                         void *stream) {
-    int rc = check_la(q, k, v, log_decay, init_state, o, final_state, cu_seqlens, B, T, H, dk, dv, num_seqs, dtype);
-    if (rc) return rc;
-    rc = check_workspace(workspace, ws_bytes,
-                         kda_la_chunk_forward_workspace_size(B, T, H, dk, dv, num_seqs, dtype, 0));
-    if (rc || num_seqs == 0) return rc;
-    cudaStream_t st = (cudaStream_t)stream;
-    if (T == 0) {
-        char msg[256] = "";
-        rc = kda::tc::state_passthrough(init_state, final_state, num_seqs, H, dk, dv, st, msg, sizeof(msg));
-        return rc ? fail(rc, "%s", msg) : KDA_OK;
-    }
-    const kda::la::Call c{cu_seqlens, nullptr, B, T, H, num_seqs, 0, log_decay, st};
-    return la_forward(c, q, k, v, init_state, o, final_state, dk, dv, dtype, workspace);
-}
-
-int kda_la_chunk_forward_slots(const void *q, const void *k, const void *v, const float *log_decay,
-                               float *state_pool, const int32_t *slots, void *o, const int32_t *cu_seqlens, int B,
-                               int T, int H, int dk, int dv, int num_seqs, int num_slots, int dtype,
-                               void *workspace, size_t ws_bytes, void *stream) {
-    int rc = check_la(q, k, v, log_decay, state_pool, o, state_pool, cu_seqlens, B, T, H, dk, dv, num_seqs, dtype);
-    if (rc) return rc;
-    if (num_seqs > 0 && (!state_pool || !slots))
-        return fail(KDA_ERR_INVALID_ARG, "state_pool and slots are required");
-    if (num_slots < 1) return fail(KDA_ERR_INVALID_ARG, "num_slots=%d must be at least 1", num_slots);
-    if (slots && !aligned(slots, 4)) return fail(KDA_ERR_MISALIGNED, "slots is not 4-byte aligned");
-    rc = check_workspace(workspace, ws_bytes,
-                         kda_la_chunk_forward_workspace_size(B, T, H, dk, dv, num_seqs, dtype, 1));
-    if (rc || num_seqs == 0 || T == 0) return rc;   // without tokens the states stay in their slots
-    const kda::la::Call c{cu_seqlens, slots, B, T, H, num_seqs, num_slots, log_decay, (cudaStream_t)stream};
-    return la_forward(c, q, k, v, state_pool, o, state_pool, dk, dv, dtype, workspace);
-}
-
-int kda_la_recurrent_step(const void *q, const void *k, const void *v, const float *log_decay, float *state, void *o,
-                          int N, int H, int dk, int dv, int dtype, void *stream) {
-    int rc = check_decode(q, k, v, log_decay, log_decay, state, o, N, H, dk, dv, dtype, true);
-    if (rc || N == 0) return rc;
-    return la_step(q, k, v, log_decay, state, o, N, H, dk, dv, dtype, nullptr, 0, (cudaStream_t)stream);
-}
-
-int kda_la_recurrent_step_slots(const void *q, const void *k, const void *v, const float *log_decay,
-                                float *state_pool, const int32_t *slots, void *o, int N, int H, int dk, int dv,
-                                int num_slots, int dtype, void *stream) {
-    int rc = check_decode(q, k, v, log_decay, log_decay, state_pool, o, N, H, dk, dv, dtype, true);
-    if (rc || N == 0) return rc;
-    if (!slots) return fail(KDA_ERR_INVALID_ARG, "slots is required");
-    if (!aligned(slots, 4)) return fail(KDA_ERR_MISALIGNED, "slots is not 4-byte aligned");
-    if (num_slots < 1) return fail(KDA_ERR_INVALID_ARG, "num_slots=%d must be at least 1", num_slots);
-    return la_step(q, k, v, log_decay, state_pool, o, N, H, dk, dv, dtype, slots, num_slots, (cudaStream_t)stream);
-}
-
-size_t kda_la_chunk_backward_workspace_size(int B, int T, int H, int dk, int dv, int num_seqs, int dtype) {
-    if (!la_sizes_ok(B, T, H, dk, dv, num_seqs, dtype) || T == 0 || num_seqs == 0) return 0;
-    return 2 * la_forward_ws(T, H, dk, dv, num_seqs, dtype, false);
-}
-
-int kda_la_chunk_backward(const void *q, const void *k, const void *v, const float *log_decay,
-                          const float *init_state, const void *d_o, const float *dfinal_state, void *dq,
-                          void *dk_out, void *dv_out, float *dinit_state, const int32_t *cu_seqlens, int B, int T,
-                          int H, int dk, int dv, int num_seqs, int dtype, void *workspace, size_t ws_bytes,
-                          void *stream) {
-    int rc = check_la(q, k, v, log_decay, init_state, d_o, dfinal_state, cu_seqlens, B, T, H, dk, dv, num_seqs, dtype);
-    if (rc) return rc;
-    if (T > 0 && (!dq || !dk_out || !dv_out)) return fail(KDA_ERR_INVALID_ARG, "dq, dk and dv are required");
-    const void *p16[] = {dq, dk_out, dv_out, dinit_state};
-    const char *n16[] = {"dq", "dk", "dv", "dinit_state"};
-    for (int i = 0; i < 4; ++i)
-        if (p16[i] && !aligned(p16[i], 16)) return fail(KDA_ERR_MISALIGNED, "%s is not 16-byte aligned", n16[i]);
-    rc = check_workspace(workspace, ws_bytes,
-                         kda_la_chunk_backward_workspace_size(B, T, H, dk, dv, num_seqs, dtype));
-    if (rc || num_seqs == 0) return rc;
-    cudaStream_t st = (cudaStream_t)stream;
-    if (T == 0) {
-        char msg[256] = "";
-        rc = kda::tc::state_passthrough(dfinal_state, dinit_state, num_seqs, H, dk, dv, st, msg, sizeof(msg));
-        return rc ? fail(rc, "%s", msg) : KDA_OK;
-    }
-    const kda::la::Call c{cu_seqlens, nullptr, B, T, H, num_seqs, 0, log_decay, st};
-    cudaError_t e = cudaErrorInvalidValue;
-#define KDA_LA(DK, DV)                                                                                             \
-    if (dk == DK && dv == DV)                                                                                      \
-        e = dtype == KDA_BF16                                                                                      \
-                ? kda::la::tc_backward<DK, DV>(c, q, k, v, d_o, init_state, dfinal_state, dq, dk_out, dv_out,      \
-                                               dinit_state, (float *)workspace)                                   \
-                : kda::la::simt_backward<DK, DV, float>(c, q, k, v, d_o, init_state, dfinal_state, dq, dk_out, dv_out, \
-                                                        dinit_state, (float *)workspace)
-    KDA_LA(64, 64);
-    KDA_LA(64, 128);
-    KDA_LA(128, 64);
-    KDA_LA(128, 128);
-#undef KDA_LA
-    return e == cudaSuccess ? KDA_OK : cuda_fail(e, "linear attention backward launch");
-}
-
-size_t kda_group_norm_workspace_size(long long N, int L, int C, int G, int dtype, int backward) {
-    if (N < 1 || L < 1 || C < 1 || G < 1 || C % G || (dtype != KDA_BF16 && dtype != KDA_F32)) return 0;
-    return kda::norm::plan_of(N, L, C, G, dtype == KDA_BF16 ? 2 : 4, backward != 0).ws;
-}
-
-int kda_group_norm_forward(const void *x, const float *weight, const float *bias, const void *gate, void *y,
-                           float *mean, float *rstd, long long N, int L, int C, int G, float eps, int act, int dtype,
-                           void *workspace, size_t ws_bytes, void *stream) {
-    int rc = check_norm(x, y, mean, rstd, weight, bias, gate, N, L, C, G, act, dtype);
-    if (rc) return rc;
-    if (!(eps > 0.f)) return fail(KDA_ERR_INVALID_ARG, "eps=%g must be above 0", (double)eps);
-    if (N == 0) return KDA_OK;
-    const int es = dtype == KDA_BF16 ? 2 : 4;
-    const kda::norm::Plan s = kda::norm::plan_of(N, L, C, G, es, false);
-    if ((rc = check_workspace(workspace, ws_bytes, s.ws))) return rc;
-    kda::norm::Args a{};
-    a.x = x; a.gate = gate; a.weight = weight; a.bias = bias; a.y = y; a.mean = mean; a.rstd = rstd; a.eps = eps;
-    a.ws = workspace;
-    const cudaError_t e = es == 2 ? kda::norm::launch<__nv_bfloat16>(s, a, act, false, (cudaStream_t)stream)
-                                  : kda::norm::launch<float>(s, a, act, false, (cudaStream_t)stream);
-    return e == cudaSuccess ? KDA_OK : cuda_fail(e, "group norm launch");
-}
-
-int kda_group_norm_backward(const void *dy, const void *x, const float *mean, const float *rstd, const float *weight,
-                            const float *bias, const void *gate, void *dx, void *dgate, float *dweight, float *dbias,
-                            long long N, int L, int C, int G, int act, int dtype, void *workspace, size_t ws_bytes,
-                            void *stream) {
-    int rc = check_norm(x, dx, mean, rstd, weight, bias, gate, N, L, C, G, act, dtype);
-    if (rc) return rc;
-    if (N == 0) {   // no samples: the sums are empty
-        const size_t bytes = (size_t)C * sizeof(float);
-        cudaError_t e = cudaSuccess;
-        if (dweight) e = cudaMemsetAsync(dweight, 0, bytes, (cudaStream_t)stream);
-        if (dbias && e == cudaSuccess) e = cudaMemsetAsync(dbias, 0, bytes, (cudaStream_t)stream);
-        return e == cudaSuccess ? KDA_OK : cuda_fail(e, "clearing dweight and dbias");
-    }
-    if (!dy) return fail(KDA_ERR_INVALID_ARG, "dy is required");
-    if (gate && !dgate) return fail(KDA_ERR_INVALID_ARG, "dgate is required with a gate");
-    if (!aligned(dy, 16) || (dgate && !aligned(dgate, 16)))
-        return fail(KDA_ERR_MISALIGNED, "dy or dgate is not 16-byte aligned");
-    if ((dweight && !aligned(dweight, 4)) || (dbias && !aligned(dbias, 4)))
-        return fail(KDA_ERR_MISALIGNED, "dweight or dbias is not 4-byte aligned");
-    const int es = dtype == KDA_BF16 ? 2 : 4;
-    const kda::norm::Plan s = kda::norm::plan_of(N, L, C, G, es, true);
-    if ((rc = check_workspace(workspace, ws_bytes, s.ws))) return rc;
-    kda::norm::Args a{};
-    a.dy = dy; a.x = x; a.gate = gate; a.weight = weight; a.bias = bias; a.y = dx; a.dgate = dgate;
-    a.mean = const_cast<float *>(mean); a.rstd = const_cast<float *>(rstd); a.dweight = dweight; a.dbias = dbias;
-    a.ws = workspace;
-    const cudaError_t e = es == 2 ? kda::norm::launch<__nv_bfloat16>(s, a, act, true, (cudaStream_t)stream)
-                                  : kda::norm::launch<float>(s, a, act, true, (cudaStream_t)stream);
-    return e == cudaSuccess ? KDA_OK : cuda_fail(e, "group norm backward launch");
-}
-
 int kda_debug_wait_timeout(long long limit_cycles, void *stream) {
     if (limit_cycles < 1 || limit_cycles > 2000000000ll)
         return fail(KDA_ERR_INVALID_ARG, "limit_cycles must lie in [1, 2e9], got %lld", limit_cycles);
@@ -1010,18 +780,22 @@ int kda_debug_wait_timeout(long long limit_cycles, void *stream) {
 int kda_get_device_status(unsigned int *bits, int clear, void *stream) {
     if (!bits) return fail(KDA_ERR_INVALID_ARG, "bits is required");
     cudaStream_t st = (cudaStream_t)stream;
-    unsigned int host = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(&host, kda::g_status, sizeof(host), 0, cudaMemcpyDeviceToHost, st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e != cudaSuccess) return cuda_fail(e, "reading the device status word");
-    if (clear && host) {
-        const unsigned int zero = 0;
-        e = cudaMemcpyToSymbolAsync(kda::g_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st);
+    unsigned int all = 0;
+    for (const StatusWord *w = kda::host::g_words; w; w = w->next) {
+        unsigned int host = 0;
+        cudaError_t e = cudaMemcpyFromSymbolAsync(&host, w->symbol, sizeof(host), 0, cudaMemcpyDeviceToHost, st);
         if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-        if (e != cudaSuccess) return cuda_fail(e, "clearing the device status word");
+        if (e != cudaSuccess) return cuda_fail(e, "reading the device status word");
+        if (clear && host) {
+            const unsigned int zero = 0;
+            e = cudaMemcpyToSymbolAsync(w->symbol, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st);
+            if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+            if (e != cudaSuccess) return cuda_fail(e, "clearing the device status word");
+        }
+        all |= host;
     }
-    *bits = host;
-    if (host) return fail(KDA_ERR_DEVICE, "device status flags 0x%x", host);
+    *bits = all;
+    if (all) return fail(KDA_ERR_DEVICE, "device status flags 0x%x", all);
     return KDA_OK;
 }
 
