@@ -77,6 +77,16 @@ __device__ __forceinline__ void store_vec(T *p, const float (&f)[VEC]) {
     *reinterpret_cast<typename Vec<T, VEC>::Raw *>(p) = Vec<T, VEC>::close(f);
 }
 
+// 16-byte access to data that is touched once.
+template <typename Raw, typename T>
+__device__ __forceinline__ Raw ld_raw(const T *p) {
+    return __ldcs(reinterpret_cast<const Raw *>(p));
+}
+template <typename Raw, typename T>
+__device__ __forceinline__ void st_raw(T *p, const Raw &v) {
+    __stcs(reinterpret_cast<Raw *>(p), v);
+}
+
 // ------------------------------------------------------------------ activations
 
 // 1 / (1 + e^-x).  The hardware exponential's error (about |x| 2^-23 relative) is far
@@ -126,15 +136,19 @@ struct RowsGeo {
     int step;         // rows between two rows of one lane group: a multiple of G
 };
 
+// Resident CTAs per SM that the rows kernels are launched and bounded for.  A lane group runs
+// over its rows with the next U rows' loads in flight behind the ones it works on.
+constexpr int rows_ctas(int nv, bool backward) {
+    return backward ? (nv == 1 ? 2 : 1) : nv == 1 ? 3 : nv == 2 ? 2 : 1;
+}
+
 // NV vectors of a row in a lane, U rows at a time.  A lane group keeps one group index g,
 // so its weights stay in registers.
 template <typename T, int NV, int U, int ACT, bool GATE>
-__global__ void __launch_bounds__(kThreads) rows_forward_kernel(RowsGeo r, const T *__restrict__ x,
-                                                                const float *__restrict__ weight,
-                                                                const float *__restrict__ bias,
-                                                                const T *__restrict__ gate, T *__restrict__ y,
-                                                                float *__restrict__ mean, float *__restrict__ rstd,
-                                                                float eps) {
+__global__ void __launch_bounds__(kThreads, rows_ctas(NV, false))
+rows_forward_kernel(RowsGeo r, const T *__restrict__ x, const float *__restrict__ weight,
+                    const float *__restrict__ bias, const T *__restrict__ gate, T *__restrict__ y,
+                    float *__restrict__ mean, float *__restrict__ rstd, float eps) {
     constexpr int VEC = vec_of<T>();
     using V = Vec<T, VEC>;
     const int per = kThreads / r.lanes;
@@ -154,25 +168,35 @@ __global__ void __launch_bounds__(kThreads) rows_forward_kernel(RowsGeo r, const
             bs[j][e] = on[j] && bias ? bias[(long long)g * r.D + d + e] : 0.f;
         }
     }
-    // whole lane groups leave the loop together with their warp's others (the bound is the warp's first row)
-    const long long warp_first = (long long)blockIdx.x * per + (threadIdx.x & ~31) / r.lanes;
-    for (long long base = 0; warp_first + base < r.rows; base += (long long)r.step * U) {
-        typename V::Raw xr[U][NV], gr[U][NV];
+    typename V::Raw xr[U][NV], gr[U][NV];
+    auto fetch = [&](long long base) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const long long row = sub + base + (long long)u * r.step;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const long long at = row * r.D + (sl + j * r.lanes) * VEC;
+                xr[u][j] = gr[u][j] = typename V::Raw();
                 if (row < r.rows && on[j]) {
-                    xr[u][j] = *reinterpret_cast<const typename V::Raw *>(x + at);
-                    if (GATE) gr[u][j] = *reinterpret_cast<const typename V::Raw *>(gate + at);
-                } else {
-                    xr[u][j] = typename V::Raw();
-                    if (GATE) gr[u][j] = typename V::Raw();
+                    xr[u][j] = ld_raw<typename V::Raw>(x + at);
+                    if (GATE) gr[u][j] = ld_raw<typename V::Raw>(gate + at);
                 }
             }
         }
+    };
+    // whole lane groups leave the loop together with their warp's others (the bound is the warp's first row)
+    const long long warp_first = (long long)blockIdx.x * per + (threadIdx.x & ~31) / r.lanes;
+    fetch(0);
+    for (long long base = 0; warp_first + base < r.rows; base += (long long)r.step * U) {
+        typename V::Raw xc[U][NV], gc[U][NV];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                xc[u][j] = xr[u][j];
+                gc[u][j] = gr[u][j];
+            }
+        fetch(base + (long long)r.step * U);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const long long row = sub + base + (long long)u * r.step;
@@ -180,7 +204,7 @@ __global__ void __launch_bounds__(kThreads) rows_forward_kernel(RowsGeo r, const
             float s = 0.f;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                V::open(xr[u][j], f[j]);
+                V::open(xc[u][j], f[j]);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) s += f[j][e];   // lanes that hold nothing add zeros
             }
@@ -199,13 +223,13 @@ __global__ void __launch_bounds__(kThreads) rows_forward_kernel(RowsGeo r, const
             for (int j = 0; j < NV; ++j) {
                 if (!on[j]) continue;
                 float gv[VEC], out[VEC];
-                if (GATE) V::open(gr[u][j], gv);
+                if (GATE) V::open(gc[u][j], gv);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     const float z = fmaf(f[j][e] * rs, wt[j][e], bs[j][e]);
                     out[e] = GATE ? z * act<T, ACT>(gv[e]) : act<T, ACT>(z);
                 }
-                store_vec<T, VEC>(y + row * r.D + (sl + j * r.lanes) * VEC, out);
+                st_raw(y + row * r.D + (sl + j * r.lanes) * VEC, V::close(out));
             }
             if (sl == 0) {
                 mean[row] = m;
@@ -217,15 +241,12 @@ __global__ void __launch_bounds__(kThreads) rows_forward_kernel(RowsGeo r, const
 
 // part: [step / G][2][C] sums of dz xhat and dz over each lane group's rows
 template <typename T, int NV, int ACT, bool GATE>
-__global__ void __launch_bounds__(kThreads) rows_backward_kernel(RowsGeo r, const T *__restrict__ dy,
-                                                                 const T *__restrict__ x,
-                                                                 const float *__restrict__ mean,
-                                                                 const float *__restrict__ rstd,
-                                                                 const float *__restrict__ weight,
-                                                                 const float *__restrict__ bias,
-                                                                 const T *__restrict__ gate, T *__restrict__ dx,
-                                                                 T *__restrict__ dgate, float *__restrict__ part) {
-    constexpr int VEC = vec_of<T>();
+__global__ void __launch_bounds__(kThreads, rows_ctas(NV, true))
+rows_backward_kernel(RowsGeo r, const T *__restrict__ dy, const T *__restrict__ x, const float *__restrict__ mean,
+                     const float *__restrict__ rstd, const float *__restrict__ weight,
+                     const float *__restrict__ bias, const T *__restrict__ gate, T *__restrict__ dx,
+                     T *__restrict__ dgate, float *__restrict__ part) {
+    constexpr int VEC = vec_of<T>(), U = NV == 1 ? 2 : 1;
     using V = Vec<T, VEC>;
     const int per = kThreads / r.lanes;
     const int sl = threadIdx.x & (r.lanes - 1);
@@ -244,55 +265,73 @@ __global__ void __launch_bounds__(kThreads) rows_backward_kernel(RowsGeo r, cons
             bs[j][e] = on[j] && bias ? bias[(long long)g * r.D + d + e] : 0.f;
         }
     }
+    struct Rows {
+        typename V::Raw x[U][NV], y[U][NV], g[U][NV];
+        float m[U], rs[U];
+    } next;
+    auto fetch = [&](long long base) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long row = sub + base + (long long)u * r.step;
+            const bool in = row < r.rows;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const long long at = row * r.D + (sl + j * r.lanes) * VEC;
+                next.x[u][j] = next.y[u][j] = next.g[u][j] = typename V::Raw();
+                if (in && on[j]) {
+                    next.x[u][j] = ld_raw<typename V::Raw>(x + at);
+                    next.y[u][j] = ld_raw<typename V::Raw>(dy + at);
+                    if (GATE) next.g[u][j] = ld_raw<typename V::Raw>(gate + at);
+                }
+            }
+            next.m[u] = in ? mean[row] : 0.f;
+            next.rs[u] = in ? rstd[row] : 0.f;
+        }
+    };
     const long long warp_first = (long long)blockIdx.x * per + (threadIdx.x & ~31) / r.lanes;
-    for (long long base = 0; warp_first + base < r.rows; base += r.step) {
-        const long long row = sub + base;
-        const bool in = row < r.rows;
-        typename V::Raw xr[NV], yr[NV], gr[NV];
+    fetch(0);
+    for (long long base = 0; warp_first + base < r.rows; base += (long long)r.step * U) {
+        const Rows cur = next;
+        fetch(base + (long long)r.step * U);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const long long at = row * r.D + (sl + j * r.lanes) * VEC;
-            xr[j] = yr[j] = gr[j] = typename V::Raw();
-            if (in && on[j]) {
-                xr[j] = *reinterpret_cast<const typename V::Raw *>(x + at);
-                yr[j] = *reinterpret_cast<const typename V::Raw *>(dy + at);
-                if (GATE) gr[j] = *reinterpret_cast<const typename V::Raw *>(gate + at);
+        for (int u = 0; u < U; ++u) {
+            const long long row = sub + base + (long long)u * r.step;
+            const bool in = row < r.rows;
+            const float m = cur.m[u], rs = cur.rs[u];
+            float xh[NV][VEC], t[NV][VEC];
+            float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                float dv[VEC], gv[VEC], dg[VEC];
+                V::open(cur.x[u][j], xh[j]);
+                V::open(cur.y[u][j], dv);
+                if (GATE) V::open(cur.g[u][j], gv);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float h = (xh[j][e] - m) * rs;
+                    const float z = fmaf(h, wt[j][e], bs[j][e]);
+                    // where there is no element dy is 0, and so is dz
+                    const float dz = back_act<T, ACT, GATE>(z, dv[e], GATE ? gv[e] : 0.f, dg[e]);
+                    xh[j][e] = h;
+                    t[j][e] = dz * wt[j][e];
+                    dw[j][e] = fmaf(dz, h, dw[j][e]);
+                    db[j][e] += dz;
+                    s1 += t[j][e];
+                    s2 = fmaf(t[j][e], h, s2);
+                }
+                if (GATE && in && on[j]) st_raw(dgate + row * r.D + (sl + j * r.lanes) * VEC, V::close(dg));
             }
-        }
-        const float m = in ? mean[row] : 0.f, rs = in ? rstd[row] : 0.f;
-        float xh[NV][VEC], t[NV][VEC];
-        float s1 = 0.f, s2 = 0.f;
+            s1 = lane_sum(s1, r.lanes) * inv;
+            s2 = lane_sum(s2, r.lanes) * inv;
+            if (!in) continue;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            float dv[VEC], gv[VEC], dg[VEC];
-            V::open(xr[j], xh[j]);
-            V::open(yr[j], dv);
-            if (GATE) V::open(gr[j], gv);
+            for (int j = 0; j < NV; ++j) {
+                if (!on[j]) continue;
+                float out[VEC];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float h = (xh[j][e] - m) * rs;
-                const float z = fmaf(h, wt[j][e], bs[j][e]);
-                // where there is no element dy is 0, and so is dz
-                const float dz = back_act<T, ACT, GATE>(z, dv[e], GATE ? gv[e] : 0.f, dg[e]);
-                xh[j][e] = h;
-                t[j][e] = dz * wt[j][e];
-                dw[j][e] = fmaf(dz, h, dw[j][e]);
-                db[j][e] += dz;
-                s1 += t[j][e];
-                s2 = fmaf(t[j][e], h, s2);
+                for (int e = 0; e < VEC; ++e) out[e] = rs * (t[j][e] - s1 - xh[j][e] * s2);
+                st_raw(dx + row * r.D + (sl + j * r.lanes) * VEC, V::close(out));
             }
-            if (GATE && in && on[j]) store_vec<T, VEC>(dgate + row * r.D + (sl + j * r.lanes) * VEC, dg);
-        }
-        s1 = lane_sum(s1, r.lanes) * inv;
-        s2 = lane_sum(s2, r.lanes) * inv;
-        if (!in) continue;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            if (!on[j]) continue;
-            float out[VEC];
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) out[e] = rs * (t[j][e] - s1 - xh[j][e] * s2);
-            store_vec<T, VEC>(dx + row * r.D + (sl + j * r.lanes) * VEC, out);
         }
     }
     const long long C = (long long)r.G * r.D;
@@ -301,9 +340,10 @@ __global__ void __launch_bounds__(kThreads) rows_backward_kernel(RowsGeo r, cons
     for (int j = 0; j < NV; ++j)
         if (on[j])
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                p[(sl + j * r.lanes) * VEC + e] = dw[j][e];
-                p[C + (sl + j * r.lanes) * VEC + e] = db[j][e];
+            for (int e = 0; e < VEC; e += 4) {
+                const int d = (sl + j * r.lanes) * VEC + e;
+                store4(p + d, make_float4(dw[j][e], dw[j][e + 1], dw[j][e + 2], dw[j][e + 3]));
+                store4(p + C + d, make_float4(db[j][e], db[j][e + 1], db[j][e + 2], db[j][e + 3]));
             }
 }
 
@@ -672,30 +712,26 @@ __global__ void __launch_bounds__(kThreads) pos_back_apply_kernel(
     }
 }
 
-// dweight, dbias from the rows form's partial sums [reps][2][C]: 32 channels a CTA.
-__global__ void __launch_bounds__(kThreads) rows_back_join_kernel(const float *__restrict__ part, int reps,
-                                                                  long long C, float *__restrict__ dweight,
-                                                                  float *__restrict__ dbias) {
-    __shared__ float2 s[kThreads / 32][32];
+// dweight (blockIdx.y 0) or dbias (1) from the rows form's partial sums [reps][2][C]: 32
+// channels a CTA, 32 warps over the partial sums.
+__global__ void __launch_bounds__(1024) rows_back_join_kernel(const float *__restrict__ part, int reps, long long C,
+                                                              float *__restrict__ dweight, float *__restrict__ dbias) {
+    __shared__ float s[32][33];
     const int lane = threadIdx.x & 31, wp = threadIdx.x / 32;
     const long long c = (long long)blockIdx.x * 32 + lane;
-    float2 v = make_float2(0.f, 0.f);
-    if (c < C)
-        for (int k = wp; k < reps; k += kThreads / 32) {
-            v.x += part[k * 2 * C + c];
-            v.y += part[(k * 2 + 1) * C + c];
-        }
+    float *dst = blockIdx.y ? dbias : dweight;
+    if (!dst) return;
+    part += blockIdx.y * C;
+    float v = 0.f;
+    if (c < C) {
+#pragma unroll 4
+        for (int k = wp; k < reps; k += 32) v += part[k * 2 * C + c];
+    }
     s[wp][lane] = v;
     __syncthreads();
-    if (wp == 0 && c < C) {
-#pragma unroll
-        for (int i = 1; i < kThreads / 32; ++i) {
-            v.x += s[i][lane].x;
-            v.y += s[i][lane].y;
-        }
-        if (dweight) dweight[c] = v.x;
-        if (dbias) dbias[c] = v.y;
-    }
+    // warp wp sums channel wp's 32 entries, in the same order every time
+    v = lane_sum(s[lane][wp], 32);
+    if (lane == 0 && (long long)blockIdx.x * 32 + wp < C) dst[(long long)blockIdx.x * 32 + wp] = v;
 }
 
 }  // namespace norm
@@ -733,8 +769,9 @@ inline Plan plan_of(long long N, int L, int C, int G, int esize, bool backward) 
         s.nv = nv <= 2 ? nv : 4;
         const long long rows = N * G, per = kThreads / lanes;
         const long long unit = G / gcd_of(G, per);   // blocks whose lane groups are a multiple of G
-        const long long want = std::min<long long>((rows + per - 1) / per, (long long)kSMs * 8);
-        s.row_blocks = (int)((want + unit - 1) / unit * unit);
+        const long long want = std::min<long long>((rows + per - 1) / per,
+                                                   (long long)kSMs * rows_ctas(s.nv, backward));
+        s.row_blocks = (int)std::max(want / unit, 1ll) * (int)unit;   // whole units, no more CTAs than fit
         s.r = RowsGeo{rows, G, D, lanes, (int)(s.row_blocks * per)};
         s.ws = backward ? (size_t)(s.r.step / G) * 2 * C * sizeof(float) : 0;
         return s;
@@ -774,8 +811,8 @@ cudaError_t launch_forward(const Plan &s, const Args &a, cudaStream_t st) {
 #define KDA_ROWS(NV, U)                                                                                         \
     rows_forward_kernel<T, NV, U, ACT, GATE><<<s.row_blocks, kThreads, 0, st>>>(s.r, x, a.weight, a.bias, gate, y, \
                                                                                 a.mean, a.rstd, a.eps)
-        if (s.nv == 1) KDA_ROWS(1, 4);
-        else if (s.nv == 2) KDA_ROWS(2, 2);
+        if (s.nv == 1) KDA_ROWS(1, 2);
+        else if (s.nv == 2) KDA_ROWS(2, 1);
         else KDA_ROWS(4, 1);
 #undef KDA_ROWS
         return cudaGetLastError();
@@ -807,8 +844,8 @@ cudaError_t launch_backward(const Plan &s, const Args &a, cudaStream_t st) {
         else KDA_ROWS(4);
 #undef KDA_ROWS
         if (a.dweight || a.dbias)
-            rows_back_join_kernel<<<(unsigned)((C + 31) / 32), kThreads, 0, st>>>(part, s.r.step / s.r.G, C, a.dweight,
-                                                                                  a.dbias);
+            rows_back_join_kernel<<<dim3((unsigned)((C + 31) / 32), 2), 1024, 0, st>>>(part, s.r.step / s.r.G, C,
+                                                                                       a.dweight, a.dbias);
         return cudaGetLastError();
     }
     const long long tiles = (long long)s.p.N * s.p.tiles;
