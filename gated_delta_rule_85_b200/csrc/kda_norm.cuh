@@ -16,6 +16,7 @@
 #include <algorithm>
 
 #include "kda_common.cuh"
+#include "tc_ptx.cuh"
 
 namespace kda {
 namespace norm {
@@ -67,6 +68,25 @@ struct Vec<float, 1> {
 };
 template <typename T>
 constexpr int vec_of() { return 16 / (int)sizeof(T); }
+// A 16-byte vector as pairs, for two operations an instruction
+template <typename T>
+__device__ __forceinline__ void open_pairs(const typename Vec<T, vec_of<T>()>::Raw &r, float2 (&f)[vec_of<T>() / 2]) {
+    float e[vec_of<T>()];
+    Vec<T, vec_of<T>()>::open(r, e);
+#pragma unroll
+    for (int i = 0; i < vec_of<T>() / 2; ++i) f[i] = make_float2(e[2 * i], e[2 * i + 1]);
+}
+template <typename T>
+__device__ __forceinline__ typename Vec<T, vec_of<T>()>::Raw close_pairs(const float2 (&f)[vec_of<T>() / 2]) {
+    float e[vec_of<T>()];
+#pragma unroll
+    for (int i = 0; i < vec_of<T>() / 2; ++i) {
+        e[2 * i] = f[i].x;
+        e[2 * i + 1] = f[i].y;
+    }
+    return Vec<T, vec_of<T>()>::close(e);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 template <typename T, int VEC>
 __device__ __forceinline__ void load_vec(const T *p, float (&f)[VEC]) {
@@ -89,12 +109,15 @@ __device__ __forceinline__ void st_raw(T *p, const Raw &v) {
 
 // ------------------------------------------------------------------ activations
 
-// 1 / (1 + e^-x).  The hardware exponential's error (about |x| 2^-23 relative) is far
-// inside a bf16 step; fp32 tensors take the full-precision one.
+// 1 / (1 + e^-x).  The hardware exponential's error (about |x| 2^-23 relative) and reciprocal's
+// are far inside a bf16 step; fp32 tensors take the full-precision exponential.
 template <typename T>
 __device__ __forceinline__ float logistic(float x) {
-    const float e = sizeof(T) == 2 ? __expf(-x) : expf(-x);
-    return __fdividef(1.f, 1.f + e);   // e = inf gives 0
+    if (sizeof(T) == 4) return __fdividef(1.f, 1.f + expf(-x));   // e = inf gives 0
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
 }
 template <typename T, int ACT>
 __device__ __forceinline__ float act(float x) {
@@ -125,6 +148,15 @@ __device__ __forceinline__ float lane_sum(float x, int lanes) {
     return x;
 }
 
+// the same over LANES lanes, unrolled; LANES = 0: `lanes`
+template <int LANES>
+__device__ __forceinline__ float group_sum(float x, int lanes) {
+    if (LANES == 0) return lane_sum(x, lanes);
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
 // ------------------------------------------------------------------ rows form
 
 constexpr int kThreads = 256;
@@ -136,102 +168,105 @@ struct RowsGeo {
     int step;         // rows between two rows of one lane group: a multiple of G
 };
 
-// Resident CTAs per SM that the rows kernels are launched and bounded for.  A lane group runs
-// over its rows with the next U rows' loads in flight behind the ones it works on.
+// Resident CTAs per SM that the rows kernels are launched and bounded for: as many as leave
+// the registers for NV vectors of every tensor.
 constexpr int rows_ctas(int nv, bool backward) {
-    return backward ? (nv == 1 ? 2 : 1) : nv == 1 ? 3 : nv == 2 ? 2 : 1;
+    return backward ? (nv == 1 ? 2 : 1) : nv == 1 ? 4 : nv == 2 ? 2 : 1;
 }
 
-// NV vectors of a row in a lane, U rows at a time.  A lane group keeps one group index g,
-// so its weights stay in registers.
-template <typename T, int NV, int U, int ACT, bool GATE>
+// What a lane keeps of its group: weights, and which of its vectors exist.
+template <typename T, int NV, int LANES>
+struct Lane {
+    static constexpr int VEC = vec_of<T>(), P = VEC / 2;
+    int sl, g, lanes, D;
+    long long sub;
+    float2 wt[NV][P], bs[NV][P];
+    __device__ __forceinline__ Lane(const RowsGeo &r, const float *weight, const float *bias)
+        : lanes(LANES ? LANES : r.lanes), D(LANES ? LANES * NV * VEC : r.D) {
+        const int per = kThreads / lanes;
+        sl = threadIdx.x & (lanes - 1);
+        sub = (long long)blockIdx.x * per + threadIdx.x / lanes;
+        g = (int)(sub % r.G);
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+                const long long c = (long long)g * D + at(j) + 2 * e;
+                wt[j][e] = on(j) && weight ? make_float2(weight[c], weight[c + 1]) : both(1.f);
+                bs[j][e] = on(j) && bias ? make_float2(bias[c], bias[c + 1]) : both(0.f);
+            }
+    }
+    __device__ __forceinline__ int at(int j) const { return (sl + j * lanes) * VEC; }
+    __device__ __forceinline__ bool on(int j) const { return LANES || at(j) < D; }
+    // the first row of the warp: whole lane groups leave a loop together with their warp's others
+    __device__ __forceinline__ long long warp_first() const {
+        return (long long)blockIdx.x * (kThreads / lanes) + (threadIdx.x & ~31) / lanes;
+    }
+};
+
+// Rows of NV vectors a lane, U at a time.  A lane group keeps one group index g, so its weights
+// stay in registers.  LANES > 0: that many lanes hold a row exactly.  Arithmetic runs in pairs:
+// at 8 bytes an element and less the instructions, not the bytes, are what takes the time
+// (36 instructions an element took 48 us where the bytes take 31).
+template <typename T, int NV, int LANES, int ACT, bool GATE>
 __global__ void __launch_bounds__(kThreads, rows_ctas(NV, false))
 rows_forward_kernel(RowsGeo r, const T *__restrict__ x, const float *__restrict__ weight,
                     const float *__restrict__ bias, const T *__restrict__ gate, T *__restrict__ y,
                     float *__restrict__ mean, float *__restrict__ rstd, float eps) {
-    constexpr int VEC = vec_of<T>();
-    using V = Vec<T, VEC>;
-    const int per = kThreads / r.lanes;
-    const int sl = threadIdx.x & (r.lanes - 1);
-    const long long sub = (long long)blockIdx.x * per + threadIdx.x / r.lanes;
-    const int g = (int)(sub % r.G);
-    const float inv = 1.f / r.D;
-    float wt[NV][VEC], bs[NV][VEC];
-    bool on[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int d = (sl + j * r.lanes) * VEC;
-        on[j] = d < r.D;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            wt[j][e] = on[j] && weight ? weight[(long long)g * r.D + d + e] : 1.f;
-            bs[j][e] = on[j] && bias ? bias[(long long)g * r.D + d + e] : 0.f;
-        }
-    }
-    typename V::Raw xr[U][NV], gr[U][NV];
-    auto fetch = [&](long long base) {
+    constexpr int U = NV == 1 ? 2 : 1, P = vec_of<T>() / 2;
+    using Raw = typename Vec<T, vec_of<T>()>::Raw;
+    const Lane<T, NV, LANES> l(r, weight, bias);
+    const float inv = 1.f / l.D;
+    for (long long base = 0; l.warp_first() + base < r.rows; base += (long long)r.step * U) {
+        Raw xr[U][NV], gr[U][NV];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const long long row = sub + base + (long long)u * r.step;
+            // behind the last row it is read again
+            const long long row = min(l.sub + base + (long long)u * r.step, r.rows - 1);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const long long at = row * r.D + (sl + j * r.lanes) * VEC;
-                xr[u][j] = gr[u][j] = typename V::Raw();
-                if (row < r.rows && on[j]) {
-                    xr[u][j] = ld_raw<typename V::Raw>(x + at);
-                    if (GATE) gr[u][j] = ld_raw<typename V::Raw>(gate + at);
+                if (!LANES) xr[u][j] = gr[u][j] = Raw();
+                if (l.on(j)) {
+                    xr[u][j] = ld_raw<Raw>(x + row * l.D + l.at(j));
+                    if (GATE) gr[u][j] = ld_raw<Raw>(gate + row * l.D + l.at(j));
                 }
             }
         }
-    };
-    // whole lane groups leave the loop together with their warp's others (the bound is the warp's first row)
-    const long long warp_first = (long long)blockIdx.x * per + (threadIdx.x & ~31) / r.lanes;
-    fetch(0);
-    for (long long base = 0; warp_first + base < r.rows; base += (long long)r.step * U) {
-        typename V::Raw xc[U][NV], gc[U][NV];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                xc[u][j] = xr[u][j];
-                gc[u][j] = gr[u][j];
-            }
-        fetch(base + (long long)r.step * U);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const long long row = sub + base + (long long)u * r.step;
-            float f[NV][VEC];
-            float s = 0.f;
+            const long long row = l.sub + base + (long long)u * r.step;
+            float2 f[NV][P], a = both(0.f);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                V::open(xc[u][j], f[j]);
+                open_pairs<T>(xr[u][j], f[j]);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) s += f[j][e];   // lanes that hold nothing add zeros
+                for (int e = 0; e < P; ++e) a = ptx::add2(a, f[j][e]);   // lanes that hold nothing add zeros
             }
-            const float m = lane_sum(s, r.lanes) * inv;
-            float q = 0.f;
+            const float m = group_sum<LANES>(a.x + a.y, l.lanes) * inv;
+            a = both(0.f);
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    f[j][e] -= m;
-                    if (on[j]) q = fmaf(f[j][e], f[j][e], q);
+                for (int e = 0; e < P; ++e) {
+                    f[j][e] = ptx::add2(f[j][e], both(-m));
+                    if (l.on(j)) a = ptx::fma2(f[j][e], f[j][e], a);
                 }
-            const float rs = rsqrtf(lane_sum(q, r.lanes) * inv + eps);
+            const float rs = rsqrtf(group_sum<LANES>(a.x + a.y, l.lanes) * inv + eps);
             if (row >= r.rows) continue;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                if (!on[j]) continue;
-                float gv[VEC], out[VEC];
-                if (GATE) V::open(gc[u][j], gv);
+                if (!l.on(j)) continue;
+                float2 gv[P], out[P];
+                if (GATE) open_pairs<T>(gr[u][j], gv);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float z = fmaf(f[j][e] * rs, wt[j][e], bs[j][e]);
-                    out[e] = GATE ? z * act<T, ACT>(gv[e]) : act<T, ACT>(z);
+                for (int e = 0; e < P; ++e) {
+                    const float2 z = ptx::fma2(ptx::mul2(f[j][e], both(rs)), l.wt[j][e], l.bs[j][e]);
+                    const float2 on = GATE ? gv[e] : z, v = make_float2(act<T, ACT>(on.x), act<T, ACT>(on.y));
+                    out[e] = GATE ? ptx::mul2(z, v) : v;
                 }
-                st_raw(y + row * r.D + (sl + j * r.lanes) * VEC, V::close(out));
+                st_raw(y + row * l.D + l.at(j), close_pairs<T>(out));
             }
-            if (sl == 0) {
+            if (l.sl == 0) {
                 mean[row] = m;
                 rstd[row] = rs;
             }
@@ -239,111 +274,113 @@ rows_forward_kernel(RowsGeo r, const T *__restrict__ x, const float *__restrict_
     }
 }
 
-// part: [step / G][2][C] sums of dz xhat and dz over each lane group's rows
-template <typename T, int NV, int ACT, bool GATE>
+// part: [step / G][2][C] sums of dz xhat and dz over each lane group's rows.  The next rows'
+// loads are in flight behind the ones it works on.
+template <typename T, int NV, int LANES, int ACT, bool GATE>
 __global__ void __launch_bounds__(kThreads, rows_ctas(NV, true))
 rows_backward_kernel(RowsGeo r, const T *__restrict__ dy, const T *__restrict__ x, const float *__restrict__ mean,
                      const float *__restrict__ rstd, const float *__restrict__ weight,
                      const float *__restrict__ bias, const T *__restrict__ gate, T *__restrict__ dx,
                      T *__restrict__ dgate, float *__restrict__ part) {
-    constexpr int VEC = vec_of<T>(), U = NV == 1 ? 2 : 1;
-    using V = Vec<T, VEC>;
-    const int per = kThreads / r.lanes;
-    const int sl = threadIdx.x & (r.lanes - 1);
-    const long long sub = (long long)blockIdx.x * per + threadIdx.x / r.lanes;
-    const int g = (int)(sub % r.G);
-    const float inv = 1.f / r.D;
-    float wt[NV][VEC], bs[NV][VEC], dw[NV][VEC] = {}, db[NV][VEC] = {};
-    bool on[NV];
+    constexpr int U = NV == 1 ? 2 : 1, P = vec_of<T>() / 2;
+    using Raw = typename Vec<T, vec_of<T>()>::Raw;
+    const Lane<T, NV, LANES> l(r, weight, bias);
+    const float inv = 1.f / l.D;
+    float2 dw[NV][P], db[NV][P];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int d = (sl + j * r.lanes) * VEC;
-        on[j] = d < r.D;
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            wt[j][e] = on[j] && weight ? weight[(long long)g * r.D + d + e] : 1.f;
-            bs[j][e] = on[j] && bias ? bias[(long long)g * r.D + d + e] : 0.f;
-        }
-    }
+        for (int e = 0; e < P; ++e) dw[j][e] = db[j][e] = both(0.f);
     struct Rows {
-        typename V::Raw x[U][NV], y[U][NV], g[U][NV];
+        Raw x[U][NV], y[U][NV], g[U][NV];
         float m[U], rs[U];
-    } next;
-    auto fetch = [&](long long base) {
+    };
+    auto fetch = [&](Rows &n, long long base) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const long long row = sub + base + (long long)u * r.step;
-            const bool in = row < r.rows;
+            const long long row = min(l.sub + base + (long long)u * r.step, r.rows - 1);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const long long at = row * r.D + (sl + j * r.lanes) * VEC;
-                next.x[u][j] = next.y[u][j] = next.g[u][j] = typename V::Raw();
-                if (in && on[j]) {
-                    next.x[u][j] = ld_raw<typename V::Raw>(x + at);
-                    next.y[u][j] = ld_raw<typename V::Raw>(dy + at);
-                    if (GATE) next.g[u][j] = ld_raw<typename V::Raw>(gate + at);
+                if (!LANES) n.x[u][j] = n.y[u][j] = n.g[u][j] = Raw();
+                if (l.on(j)) {
+                    n.x[u][j] = ld_raw<Raw>(x + row * l.D + l.at(j));
+                    n.y[u][j] = ld_raw<Raw>(dy + row * l.D + l.at(j));
+                    if (GATE) n.g[u][j] = ld_raw<Raw>(gate + row * l.D + l.at(j));
                 }
             }
-            next.m[u] = in ? mean[row] : 0.f;
-            next.rs[u] = in ? rstd[row] : 0.f;
+            n.m[u] = mean[row];
+            n.rs[u] = rstd[row];
         }
     };
-    const long long warp_first = (long long)blockIdx.x * per + (threadIdx.x & ~31) / r.lanes;
-    fetch(0);
-    for (long long base = 0; warp_first + base < r.rows; base += (long long)r.step * U) {
-        const Rows cur = next;
-        fetch(base + (long long)r.step * U);
+    auto work = [&](const Rows &c, long long base) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const long long row = sub + base + (long long)u * r.step;
+            const long long row = l.sub + base + (long long)u * r.step;
             const bool in = row < r.rows;
-            const float m = cur.m[u], rs = cur.rs[u];
-            float xh[NV][VEC], t[NV][VEC];
-            float s1 = 0.f, s2 = 0.f;
+            const float m = c.m[u], rs = c.rs[u];
+            float2 xh[NV][P], t[NV][P], s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                float dv[VEC], gv[VEC], dg[VEC];
-                V::open(cur.x[u][j], xh[j]);
-                V::open(cur.y[u][j], dv);
-                if (GATE) V::open(cur.g[u][j], gv);
+                float2 dv[P], gv[P], dg[P];
+                open_pairs<T>(c.x[u][j], xh[j]);
+                open_pairs<T>(c.y[u][j], dv);
+                if (GATE) open_pairs<T>(c.g[u][j], gv);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float h = (xh[j][e] - m) * rs;
-                    const float z = fmaf(h, wt[j][e], bs[j][e]);
-                    // where there is no element dy is 0, and so is dz
-                    const float dz = back_act<T, ACT, GATE>(z, dv[e], GATE ? gv[e] : 0.f, dg[e]);
+                for (int e = 0; e < P; ++e) {
+                    float2 h = ptx::mul2(ptx::add2(xh[j][e], both(-m)), both(rs));
+                    const float2 z = ptx::fma2(h, l.wt[j][e], l.bs[j][e]);
+                    float2 dz;
+                    if (GATE) {
+                        const float2 p = act2<T, ACT>(gv[e].x), q = act2<T, ACT>(gv[e].y);
+                        dg[e] = ptx::mul2(ptx::mul2(dv[e], z), make_float2(p.y, q.y));
+                        dz = ptx::mul2(dv[e], make_float2(p.x, q.x));
+                    } else {
+                        dz = ptx::mul2(dv[e], make_float2(act2<T, ACT>(z.x).y, act2<T, ACT>(z.y).y));
+                    }
+                    if (!in) dz = h = both(0.f);   // no row: what was read is another group's
                     xh[j][e] = h;
-                    t[j][e] = dz * wt[j][e];
-                    dw[j][e] = fmaf(dz, h, dw[j][e]);
-                    db[j][e] += dz;
-                    s1 += t[j][e];
-                    s2 = fmaf(t[j][e], h, s2);
+                    t[j][e] = ptx::mul2(dz, l.wt[j][e]);
+                    dw[j][e] = ptx::fma2(dz, h, dw[j][e]);
+                    db[j][e] = ptx::add2(db[j][e], dz);
+                    s1 = ptx::add2(s1, t[j][e]);
+                    s2 = ptx::fma2(t[j][e], h, s2);
                 }
-                if (GATE && in && on[j]) st_raw(dgate + row * r.D + (sl + j * r.lanes) * VEC, V::close(dg));
+                if (GATE && in && l.on(j)) st_raw(dgate + row * l.D + l.at(j), close_pairs<T>(dg));
             }
-            s1 = lane_sum(s1, r.lanes) * inv;
-            s2 = lane_sum(s2, r.lanes) * inv;
+            const float m1 = group_sum<LANES>(s1.x + s1.y, l.lanes) * inv;
+            const float m2 = group_sum<LANES>(s2.x + s2.y, l.lanes) * inv;
             if (!in) continue;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                if (!on[j]) continue;
-                float out[VEC];
+                if (!l.on(j)) continue;
+                float2 out[P];
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) out[e] = rs * (t[j][e] - s1 - xh[j][e] * s2);
-                st_raw(dx + row * r.D + (sl + j * r.lanes) * VEC, V::close(out));
+                for (int e = 0; e < P; ++e)
+                    out[e] = ptx::mul2(both(rs), ptx::fma2(xh[j][e], both(-m2), ptx::add2(t[j][e], both(-m1))));
+                st_raw(dx + row * l.D + l.at(j), close_pairs<T>(out));
             }
         }
+    };
+    // two sets of rows in turn, so that none is copied
+    Rows a, b;
+    const long long stride = (long long)r.step * U;
+    fetch(a, 0);
+    for (long long base = 0; l.warp_first() + base < r.rows; base += 2 * stride) {
+        fetch(b, base + stride);
+        work(a, base);
+        fetch(a, base + 2 * stride);
+        work(b, base + stride);
     }
-    const long long C = (long long)r.G * r.D;
-    float *p = part + (sub / r.G) * 2 * C + (long long)g * r.D;
+    const long long C = (long long)r.G * l.D;
+    float *p = part + (l.sub / r.G) * 2 * C + (long long)l.g * l.D;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-        if (on[j])
+        if (l.on(j))
 #pragma unroll
-            for (int e = 0; e < VEC; e += 4) {
-                const int d = (sl + j * r.lanes) * VEC + e;
-                store4(p + d, make_float4(dw[j][e], dw[j][e + 1], dw[j][e + 2], dw[j][e + 3]));
-                store4(p + C + d, make_float4(db[j][e], db[j][e + 1], db[j][e + 2], db[j][e + 3]));
+            for (int e = 0; e < P; e += 2) {
+                const int d = l.at(j) + 2 * e;
+                store4(p + d, make_float4(dw[j][e].x, dw[j][e].y, dw[j][e + 1].x, dw[j][e + 1].y));
+                store4(p + C + d, make_float4(db[j][e].x, db[j][e].y, db[j][e + 1].x, db[j][e + 1].y));
             }
 }
 
@@ -802,18 +839,30 @@ struct Args {
     void *ws;
 };
 
+// Heads of 64 and 128 channels have kernels of their own widths.
+#define KDA_ROWS_CASES                                        \
+    if (s.nv == 1) {                                          \
+        const int exact = s.r.D == s.r.lanes * VW ? s.r.lanes : 0; \
+        if (exact == 8) KDA_ROWS(1, 8);                       \
+        else if (exact == 16) KDA_ROWS(1, 16);                \
+        else if (exact == 32) KDA_ROWS(1, 32);                \
+        else KDA_ROWS(1, 0);                                  \
+    } else if (s.nv == 2) {                                   \
+        KDA_ROWS(2, 0);                                       \
+    } else {                                                  \
+        KDA_ROWS(4, 0);                                       \
+    }
+
 template <typename T, int ACT, bool GATE>
 cudaError_t launch_forward(const Plan &s, const Args &a, cudaStream_t st) {
     constexpr int VW = vec_of<T>();
     const T *x = (const T *)a.x, *gate = (const T *)a.gate;
     T *y = (T *)a.y;
     if (s.rows) {
-#define KDA_ROWS(NV, U)                                                                                         \
-    rows_forward_kernel<T, NV, U, ACT, GATE><<<s.row_blocks, kThreads, 0, st>>>(s.r, x, a.weight, a.bias, gate, y, \
-                                                                                a.mean, a.rstd, a.eps)
-        if (s.nv == 1) KDA_ROWS(1, 2);
-        else if (s.nv == 2) KDA_ROWS(2, 1);
-        else KDA_ROWS(4, 1);
+#define KDA_ROWS(NV, LANES)                                                                                     \
+    rows_forward_kernel<T, NV, LANES, ACT, GATE><<<s.row_blocks, kThreads, 0, st>>>(s.r, x, a.weight, a.bias, gate, y, \
+                                                                                    a.mean, a.rstd, a.eps)
+        KDA_ROWS_CASES
 #undef KDA_ROWS
         return cudaGetLastError();
     }
@@ -836,12 +885,10 @@ cudaError_t launch_backward(const Plan &s, const Args &a, cudaStream_t st) {
     if (s.rows) {
         float *part = (float *)a.ws;
         const long long C = (long long)s.r.G * s.r.D;
-#define KDA_ROWS(NV)                                                                                            \
-    rows_backward_kernel<T, NV, ACT, GATE><<<s.row_blocks, kThreads, 0, st>>>(s.r, dy, x, a.mean, a.rstd, a.weight, \
-                                                                              a.bias, gate, dx, dgate, part)
-        if (s.nv == 1) KDA_ROWS(1);
-        else if (s.nv == 2) KDA_ROWS(2);
-        else KDA_ROWS(4);
+#define KDA_ROWS(NV, LANES)                                                                                     \
+    rows_backward_kernel<T, NV, LANES, ACT, GATE><<<s.row_blocks, kThreads, 0, st>>>(s.r, dy, x, a.mean, a.rstd, a.weight, \
+                                                                                     a.bias, gate, dx, dgate, part)
+        KDA_ROWS_CASES
 #undef KDA_ROWS
         if (a.dweight || a.dbias)
             rows_back_join_kernel<<<dim3((unsigned)((C + 31) / 32), 2), 1024, 0, st>>>(part, s.r.step / s.r.G, C,
