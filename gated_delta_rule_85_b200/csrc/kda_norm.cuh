@@ -171,7 +171,7 @@ struct RowsGeo {
 // Resident CTAs per SM that the rows kernels are launched and bounded for: as many as leave
 // the registers for NV vectors of every tensor.
 constexpr int rows_ctas(int nv, bool backward) {
-    return backward ? (nv == 1 ? 2 : 1) : nv == 1 ? 4 : nv == 2 ? 2 : 1;
+    return backward ? (nv == 1 ? 2 : 1) : nv == 1 ? 3 : nv == 2 ? 2 : 1;
 }
 
 // What a lane keeps of its group: weights, and which of its vectors exist.
@@ -217,28 +217,32 @@ rows_forward_kernel(RowsGeo r, const T *__restrict__ x, const float *__restrict_
     using Raw = typename Vec<T, vec_of<T>()>::Raw;
     const Lane<T, NV, LANES> l(r, weight, bias);
     const float inv = 1.f / l.D;
-    for (long long base = 0; l.warp_first() + base < r.rows; base += (long long)r.step * U) {
-        Raw xr[U][NV], gr[U][NV];
+    struct Rows {
+        Raw x[U][NV], g[U][NV];
+    };
+    auto fetch = [&](Rows &n, long long base) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             // behind the last row it is read again
             const long long row = min(l.sub + base + (long long)u * r.step, r.rows - 1);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                if (!LANES) xr[u][j] = gr[u][j] = Raw();
+                if (!LANES) n.x[u][j] = n.g[u][j] = Raw();
                 if (l.on(j)) {
-                    xr[u][j] = ld_raw<Raw>(x + row * l.D + l.at(j));
-                    if (GATE) gr[u][j] = ld_raw<Raw>(gate + row * l.D + l.at(j));
+                    n.x[u][j] = ld_raw<Raw>(x + row * l.D + l.at(j));
+                    if (GATE) n.g[u][j] = ld_raw<Raw>(gate + row * l.D + l.at(j));
                 }
             }
         }
+    };
+    auto work = [&](const Rows &c, long long base) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const long long row = l.sub + base + (long long)u * r.step;
             float2 f[NV][P], a = both(0.f);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                open_pairs<T>(xr[u][j], f[j]);
+                open_pairs<T>(c.x[u][j], f[j]);
 #pragma unroll
                 for (int e = 0; e < P; ++e) a = ptx::add2(a, f[j][e]);   // lanes that hold nothing add zeros
             }
@@ -257,7 +261,7 @@ rows_forward_kernel(RowsGeo r, const T *__restrict__ x, const float *__restrict_
             for (int j = 0; j < NV; ++j) {
                 if (!l.on(j)) continue;
                 float2 gv[P], out[P];
-                if (GATE) open_pairs<T>(gr[u][j], gv);
+                if (GATE) open_pairs<T>(c.g[u][j], gv);
 #pragma unroll
                 for (int e = 0; e < P; ++e) {
                     const float2 z = ptx::fma2(ptx::mul2(f[j][e], both(rs)), l.wt[j][e], l.bs[j][e]);
@@ -271,6 +275,16 @@ rows_forward_kernel(RowsGeo r, const T *__restrict__ x, const float *__restrict_
                 rstd[row] = rs;
             }
         }
+    };
+    // two sets of rows in turn: one is in flight while the other is worked on
+    Rows a, b;
+    const long long stride = (long long)r.step * U;
+    fetch(a, 0);
+    for (long long base = 0; l.warp_first() + base < r.rows; base += 2 * stride) {
+        fetch(b, base + stride);
+        work(a, base);
+        fetch(a, base + 2 * stride);
+        work(b, base + stride);
     }
 }
 
