@@ -432,21 +432,26 @@ __device__ __forceinline__ long long part_at(const PosGeo &p, int n, int g, int 
     return (((long long)n * p.G + g) * p.tiles + tile) * p.Z + z;
 }
 
-// Chan's update: (n, mean, m2) joined with (nb, meanb, m2b)
-__device__ __forceinline__ void join_moments(float &n, float &mean, float &m2, float nb, float meanb, float m2b) {
-    if (nb == 0.f) return;
-    const float t = n + nb, d = meanb - mean, f = nb / t;
-    mean = fmaf(d, f, mean);
-    m2 += fmaf(d * d, n * f, m2b);
-    n = t;
+// Lanes that work on one of `groups` groups: all 256 threads are busy with as many at once as fit a warp's shuffles.
+__device__ __forceinline__ int lanes_for(int groups) {
+    int lanes = 32;
+    while (lanes > 1 && lanes * groups > kThreads) lanes >>= 1;
+    return lanes;
 }
-__device__ __forceinline__ void warp_join_moments(float &n, float &mean, float &m2) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        const float nb = __shfl_xor_sync(0xffffffffu, n, o), mb = __shfl_xor_sync(0xffffffffu, mean, o),
-                    qb = __shfl_xor_sync(0xffffffffu, m2, o);
-        join_moments(n, mean, m2, nb, mb, qb);
-    }
+
+// Moments pooled over `lanes` lanes: `each(f)` calls f(count, mean, m2) for the lane's parts, every
+// time the same ones.  The mean of all first, then each part's squares around it: no division
+// but one, and nothing that a large mean cancels.
+template <typename Each>
+__device__ __forceinline__ float2 pooled_moments(int lanes, float inv_count, Each &&each) {
+    float s = 0.f, q = 0.f;
+    each([&](float n, float m, float) { s = fmaf(n, m, s); });
+    const float mean = lane_sum(s, lanes) * inv_count;
+    each([&](float n, float m, float m2) {
+        const float d = m - mean;
+        q += fmaf(n * d, d, m2);
+    });
+    return make_float2(mean, lane_sum(q, lanes));
 }
 
 // Moments of a row tile and channel block for each group it touches: part[n][g][tile][z] =
@@ -499,18 +504,22 @@ __global__ void __launch_bounds__(kThreads) pos_moments_kernel(PosGeo p, const T
         }
     __syncthreads();
     const Block<VEC> b(p, z);
-    const int lane = threadIdx.x & 31;
-    for (int g = b.g0 + (int)threadIdx.x / 32; g <= b.g1; g += kThreads / 32) {
+    const int lanes = lanes_for(b.g1 - b.g0 + 1), sl = threadIdx.x & (lanes - 1);
+    // (a warp's lane groups stay together; those behind the last group work on it once more)
+    for (int g0 = b.g0 + (int)(threadIdx.x & ~31) / lanes; g0 <= b.g1; g0 += kThreads / lanes) {
+        const int g = min(g0 + (int)(threadIdx.x & 31) / lanes, b.g1);
         const int first = max(b.c0, g * p.D) - b.c0, w = channels_in<VEC>(p, z, g);
-        float c = 0.f, m = 0.f, q = 0.f;
-        for (int i = lane; i < rows * w; i += 32) {
-            const int ri = i / w, at = ri * p.tpr * VEC + first + (i - ri * w);
-            // rows of lane ri: r0 + ri, then every `rows`
-            const int have = max(0, (r1 - r0 - ri + rows - 1) / rows);
-            join_moments(c, m, q, (float)have, sm_m[at], sm_q[at]);
-        }
-        warp_join_moments(c, m, q);
-        if (lane == 0) part[part_at(p, n, g, tile, z)] = make_float2(m, q);
+        const float2 v = pooled_moments(lanes, 1.f / ((float)(r1 - r0) * w), [&](auto &&f) {
+            for (int ri = 0; ri < rows; ++ri) {
+                // rows of row lane ri: r0 + ri, then every `rows`
+                const float have = (float)max(0, (r1 - r0 - ri + rows - 1) / rows);
+                for (int c = sl; c < w; c += lanes) {
+                    const int at = ri * p.tpr * VEC + first + c;
+                    f(have, sm_m[at], sm_q[at]);
+                }
+            }
+        });
+        if (sl == 0) part[part_at(p, n, g, tile, z)] = v;
     }
 }
 
@@ -527,21 +536,27 @@ __global__ void __launch_bounds__(kThreads) pos_apply_kernel(PosGeo p, const T *
     __shared__ float2 stat[VEC * kThreads];   // (mean, rstd) of the block's groups
     const int tile = blockIdx.x % p.tiles, n = blockIdx.x / p.tiles, z = blockIdx.y;
     const Block<VEC> b(p, z);
-    const int lane = threadIdx.x & 31;
-    for (int g = b.g0 + (int)threadIdx.x / 32; g <= b.g1; g += kThreads / 32) {
+    const int lanes = lanes_for(b.g1 - b.g0 + 1), sl = threadIdx.x & (lanes - 1);
+    for (int g0 = b.g0 + (int)(threadIdx.x & ~31) / lanes; g0 <= b.g1; g0 += kThreads / lanes) {
+        const int g = min(g0 + (int)(threadIdx.x & 31) / lanes, b.g1);
         const int z0 = g * p.D / (p.tpr * VEC), zn = ((g + 1) * p.D - 1) / (p.tpr * VEC) - z0 + 1;
-        float c = 0.f, m = 0.f, q = 0.f;
-        for (int i = lane; i < p.tiles * zn; i += 32) {
-            const int t = i / zn, zz = z0 + i - t * zn;
-            const float2 v = part[part_at(p, n, g, t, zz)];
-            join_moments(c, m, q, (float)p.rows_of(t) * channels_in<VEC>(p, zz, g), v.x, v.y);
-        }
-        warp_join_moments(c, m, q);
-        const float rs = rsqrtf(q / c + eps);
-        if (lane == 0) {
-            stat[g - b.g0] = make_float2(m, rs);
+        const float inv = 1.f / ((float)p.L * p.D);
+        const float2 v = pooled_moments(lanes, inv, [&](auto &&f) {
+            for (int zz = z0; zz < z0 + zn; ++zz) {
+                const float w = (float)channels_in<VEC>(p, zz, g);
+                const float2 *at = part + part_at(p, n, g, 0, zz);
+#pragma unroll 4
+                for (int t = sl; t < p.tiles; t += lanes) {
+                    const float2 u = at[(long long)t * p.Z];
+                    f(w * p.rows_of(t), u.x, u.y);
+                }
+            }
+        });
+        if (sl == 0) {
+            const float rs = rsqrtf(v.y * inv + eps);
+            stat[g - b.g0] = make_float2(v.x, rs);
             if (tile == 0 && z == z0) {
-                mean[(long long)n * p.G + g] = m;
+                mean[(long long)n * p.G + g] = v.x;
                 rstd[(long long)n * p.G + g] = rs;
             }
         }
@@ -665,18 +680,19 @@ __global__ void __launch_bounds__(kThreads) pos_back_sums_kernel(
         sm_b[i] = v.y;
     }
     __syncthreads();
-    const int lane = threadIdx.x & 31;
-    for (int g = b.g0 + (int)threadIdx.x / 32; g <= b.g1; g += kThreads / 32) {
+    const int lanes = lanes_for(b.g1 - b.g0 + 1), sl = threadIdx.x & (lanes - 1);
+    for (int g0 = b.g0 + (int)(threadIdx.x & ~31) / lanes; g0 <= b.g1; g0 += kThreads / lanes) {
+        const int g = min(g0 + (int)(threadIdx.x & 31) / lanes, b.g1);
         const int first = max(b.c0, g * p.D), w = channels_in<VEC>(p, z, g);
         float s1 = 0.f, s2 = 0.f;
-        for (int i = lane; i < w; i += 32) {
+        for (int i = sl; i < w; i += lanes) {
             const float wt = weight ? weight[first + i] : 1.f;
             s1 = fmaf(wt, sm_b[first - b.c0 + i], s1);
             s2 = fmaf(wt, sm_w[first - b.c0 + i], s2);
         }
-        s1 = lane_sum(s1, 32);
-        s2 = lane_sum(s2, 32);
-        if (lane == 0) part[part_at(p, n, g, tile, z)] = make_float2(s1, s2);
+        s1 = lane_sum(s1, lanes);
+        s2 = lane_sum(s2, lanes);
+        if (sl == 0) part[part_at(p, n, g, tile, z)] = make_float2(s1, s2);
     }
 }
 
@@ -715,18 +731,23 @@ __global__ void __launch_bounds__(kThreads) pos_back_apply_kernel(
     const int tile = blockIdx.x % p.tiles, n = blockIdx.x / p.tiles, z = blockIdx.y;
     const Block<VEC> b(p, z);
     const float inv = 1.f / ((float)p.L * p.D);
-    for (int g = b.g0 + (int)threadIdx.x / 32; g <= b.g1; g += kThreads / 32) {
+    const int lanes = lanes_for(b.g1 - b.g0 + 1), sl = threadIdx.x & (lanes - 1);
+    for (int g0 = b.g0 + (int)(threadIdx.x & ~31) / lanes; g0 <= b.g1; g0 += kThreads / lanes) {
+        const int g = min(g0 + (int)(threadIdx.x & 31) / lanes, b.g1);
         const int z0 = g * p.D / (p.tpr * VEC), zn = ((g + 1) * p.D - 1) / (p.tpr * VEC) - z0 + 1;
         float s1 = 0.f, s2 = 0.f;
-        for (int i = lane; i < p.tiles * zn; i += 32) {
-            const int t = i / zn;
-            const float2 v = part[part_at(p, n, g, t, z0 + i - t * zn)];
-            s1 += v.x;
-            s2 += v.y;
+        for (int zz = z0; zz < z0 + zn; ++zz) {
+            const float2 *at = part + part_at(p, n, g, 0, zz);
+#pragma unroll 4
+            for (int t = sl; t < p.tiles; t += lanes) {
+                const float2 v = at[(long long)t * p.Z];
+                s1 += v.x;
+                s2 += v.y;
+            }
         }
-        s1 = lane_sum(s1, 32);
-        s2 = lane_sum(s2, 32);
-        if (lane == 0) stat[g - b.g0] = make_float2(s1 * inv, s2 * inv);
+        s1 = lane_sum(s1, lanes);
+        s2 = lane_sum(s2, lanes);
+        if (sl == 0) stat[g - b.g0] = make_float2(s1 * inv, s2 * inv);
     }
     __syncthreads();
     const int rl = threadIdx.x / p.tpr, cl = threadIdx.x % p.tpr, rows = kThreads / p.tpr;
