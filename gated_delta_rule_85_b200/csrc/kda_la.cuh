@@ -40,10 +40,12 @@ struct Geo {
     const int32_t *cu;   // packed offsets, or null
     int T, N, H;         // tokens of a row (packed: of the call), sequences, heads
     int nslots;          // chunk slots of one head
-    int W;               // spans
+    int W;               // spans: `rem` of them have per + 1 items, the others per
+    int rem;
+    long long per;
     __host__ __device__ long long items() const { return (long long)H * nslots; }
-    __host__ __device__ long long lo(int w) const { return items() * w / W; }
-    __host__ __device__ long long hi(int w) const { return items() * (w + 1) / W; }
+    __host__ __device__ long long lo(int w) const { return w * per + (w < rem ? w : rem); }
+    __host__ __device__ long long hi(int w) const { return lo(w + 1); }
 };
 
 // Where one item lies.  seek and step are warp-collective (all 32 lanes, converged).
@@ -58,7 +60,15 @@ struct Cursor {
         return min(max(g.cu[n], 0), g.T) / C + n;
     }
 
-    __device__ void seek(const Geo &g, long long u) {
+    // Not inlined, as it runs once a sequence and every copy of it takes room from the kernels'
+    // loops; it fills another cursor, so that this one stays in registers.
+    __device__ __forceinline__ void seek(const Geo &g, long long u) {
+        Cursor c;
+        find(g, u, c);
+        *this = c;
+    }
+    __device__ __noinline__ static void find(const Geo &g, long long u, Cursor &c) { c.find_item(g, u); }
+    __device__ __forceinline__ void find_item(const Geo &g, long long u) {
         h = (int)(u / g.nslots);
         slot = (int)(u - (long long)h * g.nslots);
         if (!g.cu) {
@@ -108,8 +118,9 @@ struct Cursor {
 // exp(log_decay e) with the exponent's product in 64 bits, as the sum of two floats:
 // a chunk's decay is applied once per chunk of a sequence, so an error in its last
 // place would grow with the number of chunks.
+__device__ __noinline__ double exp64(double x) { return exp(x); }   // one copy in a kernel
 __device__ __forceinline__ float2 decay2(float log_decay, double e) {
-    const double x = exp((double)log_decay * e);
+    const double x = exp64((double)log_decay * e);
     const float hi = (float)x;
     return make_float2(hi, (float)(x - (double)hi));
 }

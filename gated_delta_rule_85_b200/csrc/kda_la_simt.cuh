@@ -272,9 +272,11 @@ struct Call {
 
 template <int C>
 Geo geo_of(const Call &c) {
-    Geo g{c.cu, c.T, c.N, c.H, 0, 0};
+    Geo g{c.cu, c.T, c.N, c.H, 0, 0, 0, 0};
     g.nslots = (int)(c.cu ? (long long)c.T / C + c.N : (long long)c.N * ((c.T + C - 1) / C));
     g.W = (int)std::min<long long>(g.items(), kSMs);
+    g.per = g.items() / g.W;
+    g.rem = (int)(g.items() % g.W);
     return g;
 }
 

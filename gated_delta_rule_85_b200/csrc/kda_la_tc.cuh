@@ -17,6 +17,8 @@
 // the states of cut ones are made by the first pass and the join.
 #pragma once
 
+#include <type_traits>
+
 #include "kda_la.cuh"
 #include "tc_ptx.cuh"
 #include "tc_tile.cuh"
@@ -26,7 +28,8 @@ namespace la {
 
 constexpr int kC = 128;                  // tokens of a chunk
 constexpr int kBox = 64;                 // token rows of a TMA box
-constexpr int kSumThreads = 320;         // producer warp, MMA warp, eight compute warps
+constexpr int kSumWarps = 8;                        // split warps of the first pass, and as many that add up
+constexpr int kSumThreads = 64 + 2 * kSumWarps * 32;   // producer, MMA, split, sum
 constexpr int kStateWarps = 8;
 constexpr int kWalkThreads = 192 + kStateWarps * 32;   // producer, MMA, four output warps, state warps
 constexpr int kOutBox = 32;              // token rows of an output box: one warp's
@@ -59,44 +62,51 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 // 16-byte group g of row r in a 128-byte-swizzled atom (64 bf16 wide)
 __device__ __forceinline__ uint32_t swz(int r, int g) { return (uint32_t)(r * 128 + ((g ^ (r & 7)) << 4)); }
 
-// A weight as bf16 terms that sum to it (24 bits), each twice.
+// A token's weight, and its leading two bf16 terms, each twice.
 struct Weight {
-    __nv_bfloat162 w0, w1, w2;
-    __device__ __forceinline__ explicit Weight(float w) {
-        const float a = __bfloat162float(__float2bfloat16_rn(w)), b = __bfloat162float(__float2bfloat16_rn(w - a));
+    float w;
+    __nv_bfloat162 w0, w1;
+    __device__ __forceinline__ explicit Weight(float x) : w(x) {
+        const float a = __bfloat162float(__float2bfloat16_rn(x));
         w0 = __float2bfloat162_rn(a);
-        w1 = __float2bfloat162_rn(b);
-        w2 = __float2bfloat162_rn(w - a - b);
+        w1 = __float2bfloat162_rn(x - a);
     }
 };
+__device__ __forceinline__ float lo_bf16(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+// upper halves of two fp32 as two bf16, and what is left without them
+__device__ __forceinline__ uint32_t tops(float2 a) {
+    return __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x7632);
+}
+__device__ __forceinline__ float2 rest(float2 a) {
+    return ptx::add2(a, make_float2(-hi_bf16(__float_as_uint(a.x)), -hi_bf16(__float_as_uint(a.y))));
+}
 
-// Eight weighted elements as bf16 terms, largest first, in bf16 arithmetic two at a time (a
-// third of the instructions of the same in fp32, and no conversions).  A product of two bf16
-// numbers is the sum of its rounding and a residual that fused multiply-add gives exactly:
-//   w0 x = t0 + r,  w1 x = p + q,  t1 = round(r + p),  t2 = (r + p - t1) + q + w2 x
-// with r + p - t1 exact by the two-sum.  What is dropped is below 2^-25 of w x; with two
-// terms, t1 = round(w1 x + r), below 2^-16.
+// Eight weighted elements as bf16 terms, largest first.
+// Three: the 24 bits of the fp32 product, cut in three without an error.  (In bf16 arithmetic,
+// with residuals by fused multiply-adds and a two-sum, 12 instructions a pair, a 64-token tile
+// took 1.6k cycles: bf16 arithmetic runs at a fraction of the rate of moves and fp32.)
+// Two: w0 x = t0 + r exactly, by a fused multiply-add, and t1 = round(w1 x + r); what is
+// dropped is below 2^-16 of w x.
 template <bool THREE>
 __device__ __forceinline__ void split8(const uint4 &x, const Weight &w, uint4 &t0, uint4 &t1, uint4 &t2) {
     const uint32_t in[4] = {x.x, x.y, x.z, x.w};
     uint32_t o[3][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162 *>(&in[i]);
-        const __nv_bfloat162 a = __hmul2_rn(w.w0, v), r = __hfma2(w.w0, v, __hneg2(a));
-        __nv_bfloat162 b, c = __nv_bfloat162();
         if (THREE) {
-            const __nv_bfloat162 p = __hmul2_rn(w.w1, v), q = __hfma2(w.w1, v, __hneg2(p));
-            b = __hadd2_rn(r, p);
-            const __nv_bfloat162 z = __hsub2_rn(b, r);
-            const __nv_bfloat162 e = __hadd2_rn(__hsub2_rn(r, __hsub2_rn(b, z)), __hsub2_rn(p, z));
-            c = __hadd2_rn(e, __hfma2(w.w2, v, q));
+            const float2 a = ptx::mul2(make_float2(lo_bf16(in[i]), hi_bf16(in[i])), make_float2(w.w, w.w));
+            const float2 b = rest(a), c = rest(b);
+            o[0][i] = tops(a);
+            o[1][i] = tops(b);
+            o[2][i] = tops(c);
         } else {
-            b = __hfma2(w.w1, v, r);
+            const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162 *>(&in[i]);
+            const __nv_bfloat162 a = __hmul2_rn(w.w0, v), b = __hfma2(w.w1, v, __hfma2(w.w0, v, __hneg2(a)));
+            o[0][i] = *reinterpret_cast<const uint32_t *>(&a);
+            o[1][i] = *reinterpret_cast<const uint32_t *>(&b);
+            o[2][i] = 0u;
         }
-        o[0][i] = *reinterpret_cast<const uint32_t *>(&a);
-        o[1][i] = *reinterpret_cast<const uint32_t *>(&b);
-        o[2][i] = *reinterpret_cast<const uint32_t *>(&c);
     }
     t0 = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
     t1 = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
@@ -112,13 +122,15 @@ __device__ __forceinline__ void split8(const uint4 &x, const Weight &w, uint4 &t
 // the far end towards the near one, against the walk, and takes the far part first, so that
 // what the walk reads first is what L2 saw last.
 //
-// A tile's three-term products leave TMEM after 12 K steps and are added in fp32 registers,
-// scaled by the decay of the tokens behind the tile, so that neither the tensor core's
+// Weighted rows are three terms where these sums can become a state that the caller gets (asked
+// for or not: the outputs do not depend on that), else two.  A tile's products
+// leave TMEM after 8 or 12 K steps and are added in fp32 registers, scaled by the decay of the tokens behind the tile, so that neither the tensor core's
 // accumulation nor a product of many decays costs fp32 accuracy over long sequences.
 struct SumRole {
     CUtensorMap b, c;
     float *sum_in, *sum_out;
     int dir;
+    int three;          // terms of a weighted row: three, or two
     int want_last;
 };
 struct SumArgs {
@@ -132,7 +144,7 @@ struct SumSmem {
     static constexpr int NST = 4;
     static constexpr int E = NST * STAGE;                // [2][middle, low] terms of c
     static constexpr int BAR = E + 2 * 2 * CT;
-    static constexpr int BYTES = BAR + 8 * (2 * NST + 2 + 1) + 16;
+    static constexpr int BYTES = BAR + 8 * (2 * NST + 4 + 1) + 16;
     static constexpr int ALLOC = BYTES + 1024;
     static_assert(ALLOC <= 232448, "shared memory");
 };
@@ -146,8 +158,8 @@ la_sum_kernel(const __grid_constant__ SumArgs args, Geo g, const float *__restri
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sb = ptx::smem_u32(sm);
     const uint32_t bar_full = sb + L::BAR, bar_done = bar_full + 8 * NST, bar_ready = bar_done + 8 * NST,
-                   bar_fin = bar_ready + 16;
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::BAR + 8 * (2 * NST + 3));
+                   bar_added = bar_ready + 16, bar_fin = bar_added + 16;
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::BAR + 8 * (2 * NST + 5));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const SumRole &role = args.role[blockIdx.y];
     const int dir = role.dir, w = blockIdx.x;
@@ -203,8 +215,10 @@ la_sum_kernel(const __grid_constant__ SumArgs args, Geo g, const float *__restri
             ptx::mbar_init(bar_full + 8 * s, 1);
             ptx::mbar_init(bar_done + 8 * s, 1);
         }
-        ptx::mbar_init(bar_ready, 8);
-        ptx::mbar_init(bar_ready + 8, 8);
+        for (int s = 0; s < 2; ++s) {
+            ptx::mbar_init(bar_ready + 8 * s, kSumWarps);
+            ptx::mbar_init(bar_added + 8 * s, kSumWarps);
+        }
         ptx::mbar_init(bar_fin, 1);
         ptx::fence_mbar_init();
     }
@@ -245,13 +259,15 @@ la_sum_kernel(const __grid_constant__ SumArgs args, Geo g, const float *__restri
         for (int n = 0; n < nt; ++n) {
             const int s = n % NST, e = n & 1;
             ok = wait_warp(bar_full + 8 * s, (uint32_t)((n / NST) & 1)) &&
-                 wait_warp(bar_ready + 8 * e, (uint32_t)((n >> 1) & 1));
+                 wait_warp(bar_ready + 8 * e, (uint32_t)((n >> 1) & 1)) &&
+                 (n < 2 || wait_warp(bar_added + 8 * e, (uint32_t)(((n >> 1) - 1) & 1)));
             if (!ok) break;
             ptx::tc_fence_after();
             if (lane == 0) {
                 const uint32_t bt = sb + s * L::STAGE;
 #pragma unroll
                 for (int p = 0; p < 3; ++p) {
+                    if (p == 2 && !role.three) break;
                     const uint32_t ct = p == 0 ? bt + L::BT : sb + L::E + (e * 2 + p - 1) * L::CT;
 #pragma unroll
                     for (int ks = 0; ks < kBox / 16; ++ks)
@@ -268,32 +284,73 @@ la_sum_kernel(const __grid_constant__ SumArgs args, Geo g, const float *__restri
         }
         __syncwarp();
         wait_warp(bar_fin, 0u);
-    } else {
-        // ---------------- compute: split the weighted rows; thread <-> state row, half of its columns
-        constexpr int CPT = DC / 2;
-        const int ct = tid - 64, quad = warp & 3, half = (warp - 2) >> 2;
-        const int jr = ct & 63, jq = ct >> 6;     // split: token row, quarter of the columns
-        const int row = quad * 32 + lane, col = half * CPT;
-        const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16) + col;
-        auto wait_sum = [&](uint32_t bar, uint32_t parity) { return wait_group<1, 256>(warp == 2, bar, parity); };
-        float S[CPT];
-        float scale[2] = {};         // decay of the tokens behind the two tiles in flight
-        auto drain = [&](int x) {    // adds tile x's sum
-            if (!(ok = wait_sum(bar_done + 8 * (x % NST), (uint32_t)((x / NST) & 1)))) return;
-            ptx::tc_fence_after();
-            if (quad * 32 < DB) {
-                const uint32_t u = tl + (x & 1) * 128;
-                const float sc = x & 1 ? scale[1] : scale[0];
-#pragma unroll
-                for (int k = 0; k < CPT / 32; ++k) {
-                    float v[32];
-                    ptx::tmem_ld32(u + 32 * k, v);
-                    ptx::tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) S[32 * k + i] = fmaf(sc, v[i], S[32 * k + i]);
-                }
-            }
+    } else if (warp < 2 + kSumWarps) {
+        // ---------------- split the weighted rows.  Thread <-> token row, a part of its columns.
+        constexpr int JP = kSumWarps / 2, CG = DC / 8 / JP, BG = DB / 8 / JP;   // 16-byte groups
+        const int ct = tid - 64, jr = ct & 63, jq = ct >> 6;
+        auto wait_split = [&](uint32_t bar, uint32_t parity) {
+            return wait_group<1, kSumWarps * 32>(warp == 2, bar, parity);
         };
+        int n = 0;
+#pragma unroll 1
+        for (int q = 0; q < 2 && ok; ++q) {
+            const Part &p = part[q];
+            if (p.nt == 0) continue;
+            const double lg = (double)log_decay[p.h];
+            // forwards the weight counts from the tile's end, backwards from its start
+            const Weight full_wt((float)exp64(lg * (dir > 0 ? kBox - 1 - jr : jr + 1)));
+#pragma unroll 1
+            for (int x = 0; x < p.nt; ++x, ++n) {
+                const int s = n % NST, e = n & 1;
+                // the tile is there, and the smaller terms' buffer was multiplied
+                ok = wait_split(bar_full + 8 * s, (uint32_t)((n / NST) & 1)) &&
+                     (n < 2 || wait_split(bar_done + 8 * ((n - 2) % NST), (uint32_t)(((n - 2) / NST) & 1)));
+                if (!ok) break;
+                const int len = (int)min((long long)kBox, p.tb - tile_tok(p, x));
+                const uint32_t bt = sb + s * L::STAGE, c0 = bt + L::BT;
+                const uint32_t c1 = sb + L::E + e * 2 * L::CT, c2 = c1 + L::CT;
+                const bool live = jr < len;
+                Weight wt = full_wt;
+                if (len < kBox && dir > 0) wt = Weight(live ? (float)exp64(lg * (len - 1 - jr)) : 0.f);
+                uint4 v[CG];   // the row's groups
+                uint32_t at[CG];
+#pragma unroll
+                for (int k = 0; k < CG; ++k) {
+                    const int cg = jq * CG + k;
+                    at[k] = (cg >> 3) * 8192 + swz(jr, cg & 7);
+                    v[k] = ptx::lds128(c0 + at[k]);
+                    if (!live) v[k] = make_uint4(0, 0, 0, 0);   // rows behind the end may hold anything
+                }
+                auto put = [&](auto three) {
+#pragma unroll
+                    for (int k = 0; k < CG; ++k) {
+                        uint4 t0, t1, t2;
+                        split8<decltype(three)::value>(v[k], wt, t0, t1, t2);
+                        ptx::sts128(c0 + at[k], t0);
+                        ptx::sts128(c1 + at[k], t1);
+                        if (decltype(three)::value) ptx::sts128(c2 + at[k], t2);
+                    }
+                };
+                if (role.three) put(std::true_type());
+                else put(std::false_type());
+                if (!live)
+#pragma unroll
+                    for (int k = 0; k < BG; ++k) {
+                        const int cg = jq * BG + k;
+                        ptx::sts128(bt + (cg >> 3) * 8192 + swz(jr, cg & 7), 0, 0, 0, 0);
+                    }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar_ready + 8 * e);
+            }
+        }
+        if (!ok && lane == 0) flag_status(KDA_DEV_WAIT_TIMEOUT);
+    } else {
+        // ---------------- add up the tiles' sums.  Thread <-> state row, half of its columns.
+        constexpr int CPT = DC / (kSumWarps / 4);
+        const int quad = warp & 3, row = quad * 32 + lane, col = ((warp - 2 - kSumWarps) >> 2) * CPT;
+        const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16) + col;
+        float S[CPT];
         int n = 0;
 #pragma unroll 1
         for (int q = 0; q < 2 && ok; ++q) {
@@ -301,50 +358,32 @@ la_sum_kernel(const __grid_constant__ SumArgs args, Geo g, const float *__restri
             if (p.nt == 0) continue;
 #pragma unroll
             for (int x = 0; x < CPT; ++x) S[x] = 0.f;
-            const double lg = (double)log_decay[p.h];
-            const double full_dec = exp(lg * kBox);
-            double behind = 1.0;
-            // forwards the weight counts from the tile's end, backwards from its start
-            const Weight full_wt((float)exp(lg * (dir > 0 ? kBox - 1 - jr : jr + 1)));
+            const double lg = (double)log_decay[p.h], full_dec = exp64(lg * kBox);
+            double behind = 1.0;         // decay of the tokens behind the tile
 #pragma unroll 1
             for (int x = 0; x < p.nt; ++x, ++n) {
-                const int s = n % NST, e = n & 1;
-                // the middle and low terms' buffer is free: tile n - 2 was drained
-                if (!(ok = wait_sum(bar_full + 8 * s, (uint32_t)((n / NST) & 1)))) break;
                 const int len = (int)min((long long)kBox, p.tb - tile_tok(p, x));
-                const uint32_t bt = sb + s * L::STAGE, c0 = bt + L::BT;
-                const uint32_t c1 = sb + L::E + e * 2 * L::CT, c2 = c1 + L::CT;
-                const bool live = jr < len;
-                Weight wt = full_wt;
-                if (len < kBox && dir > 0) wt = Weight(live ? (float)exp(lg * (len - 1 - jr)) : 0.f);
+                const float sc = (float)behind;
+                behind *= len == kBox ? full_dec : exp64(lg * len);
+                ok = wait_group<2, kSumWarps * 32>(warp == 2 + kSumWarps, bar_done + 8 * (n % NST),
+                                                   (uint32_t)((n / NST) & 1));
+                if (!ok) break;
+                ptx::tc_fence_after();
+                if (quad * 32 < DB) {
+                    const uint32_t u = tl + (n & 1) * 128;
 #pragma unroll
-                for (int k = 0; k < DC / 32; ++k) {
-                    const int cg = jq * (DC / 32) + k;   // 16-byte group of the row
-                    const uint32_t at = (cg >> 3) * 8192 + swz(jr, cg & 7);
-                    uint4 t0 = make_uint4(0, 0, 0, 0), t1 = t0, t2 = t0;   // rows behind the end may hold anything
-                    if (live) split8<true>(ptx::lds128(c0 + at), wt, t0, t1, t2);
-                    ptx::sts128(c0 + at, t0);
-                    ptx::sts128(c1 + at, t1);
-                    ptx::sts128(c2 + at, t2);
-                }
-                if (!live)
+                    for (int k = 0; k < CPT / 16; ++k) {
+                        float v[16];
+                        ptx::tmem_ld16(u + 16 * k, v);
+                        ptx::tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < DB / 32; ++k) {
-                        const int cg = jq * (DB / 32) + k;
-                        ptx::sts128(bt + (cg >> 3) * 8192 + swz(jr, cg & 7), 0, 0, 0, 0);
+                        for (int i = 0; i < 16; ++i) S[16 * k + i] = fmaf(sc, v[i], S[16 * k + i]);
                     }
-                if (e) scale[1] = (float)behind;
-                else scale[0] = (float)behind;
-                behind *= len == kBox ? full_dec : exp(lg * len);
-                ptx::fence_proxy_async_smem();
+                }
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar_ready + 8 * e);
-                if (x > 0) drain(n - 1);   // the tile before, while this one multiplies
-                if (!ok) break;
+                if (lane == 0) ptx::mbar_arrive(bar_added + 8 * (n & 1));
             }
-            if (!ok) break;
-            drain(n - 1);
             if (ok && row < DB) {
                 float *dst = (p.in ? role.sum_in : role.sum_out) + ((long long)w * DB + row) * DC + col;
 #pragma unroll
@@ -408,6 +447,7 @@ struct WalkRole {
     __nv_bfloat16 *out;
     Carry y;
     int dir;
+    int three;          // states of whole sequences are the caller's: three terms (asked for or not)
     int transposed;     // the carried states are [DC][DAB]; y.last is null then
 };
 struct WalkArgs {
@@ -492,7 +532,28 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
     int n = 0;   // chunks so far
 
     if (warp == 0) {
-        // ---------------- producer
+        // ---------------- producer, and the sender of outputs
+        int meta[NST][3] = {};   // lane 0: first token, head and length of the chunks in flight
+        // The output rows of chunk k are in its tile: send the whole boxes, and wait until they are read.
+        // (A box in which a sequence ends was written by its warp: the rows behind it are not its.)
+        auto send = [&](int k) {
+            const int s = k % NST;
+            if (!wait_warp(bar_out + 8 * s, (uint32_t)((k / NST) & 1))) return false;
+            if (lane == 0) {
+#pragma unroll
+                for (int x = 0; x < NST; ++x)
+                    if (x == s)
+                        for (int q = 0; q * kOutBox + kOutBox <= meta[x][2]; ++q)
+#pragma unroll
+                            for (int a = 0; a < DC / 64; ++a)
+                                ptx::tma_store_3d(&role.out_map, sb + L::ST0 + s * L::STAGE + a * 16384 + q * kOutBox * 128,
+                                                  a * 64, meta[x][1], meta[x][0] + q * kOutBox);
+                ptx::bulk_commit();
+                ptx::bulk_wait_read_all();
+            }
+            __syncwarp();
+            return true;
+        };
         while (it.next(g)) {
             const int s = n % NST;
             const uint32_t bar = bar_full + 8 * s, dst = sb + L::ST0 + s * L::STAGE, old = (uint32_t)((n / NST - 1) & 1);
@@ -512,16 +573,20 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
                 load(&role.c, dst + 2 * L::AT, DC / 64);
             }
             __syncwarp();
-            ok = n < NST || wait_warp(bar_out + 8 * s, old);
+            if (n >= NST) ok = send(n - NST);
             // (after a wait that ran out the rest is loaded all the same: the barrier has counted it)
             if (lane == 0) {
                 load(&role.a, dst, DAB / 64);
                 if (!B_EARLY) load(&role.b, dst + L::AT, DAB / 64);
+                meta[n % NST][0] = t;
+                meta[n % NST][1] = h;
+                meta[n % NST][2] = len;
             }
             __syncwarp();
             ++n;
             if (!ok) break;
         }
+        for (int k = max(0, n - NST); k < n && ok; ++k) ok = send(k);
         if (!ok) {
             if (lane == 0) flag_status(KDA_DEV_WAIT_TIMEOUT);
             for (int k = max(0, n - NST); k < n; ++k)   // copies in flight
@@ -531,61 +596,54 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
         // ---------------- MMA
         constexpr uint32_t id_sc = ptx::idesc_bf16_f32(128, 128), id_in = ptx::idesc_bf16_f32(128, DC, false, true),
                            id_u = ptx::idesc_bf16_f32(128, DC, true, true);
+        const uint32_t me = lane == 0 ? 1u : 0u;
+        // (values that a shuffle hands round are uniform to the compiler)
+        const uint32_t sbu = __shfl_sync(0xffffffffu, sb, 0), tmu = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint32_t u_sc = tmu, u_oa = tmu + 128, u_oi = tmu + 256, u_u = tmu + 384;
         while (it.next(g)) {
-            const int s = n % NST;
-            const uint32_t at = sb + L::ST0 + s * L::STAGE, bt = at + L::AT, ct = bt + L::AT, ph = (uint32_t)(n & 1);
+            const int s = __shfl_sync(0xffffffffu, n % NST, 0);
+            const uint32_t at = sbu + L::ST0 + s * L::STAGE, bt = at + L::AT, ct = bt + L::AT, ph = (uint32_t)(n & 1);
             // scores: the region is free once the chunk before has multiplied its P
             ok = wait_warp(bar_full + 8 * s, (uint32_t)((n / NST) & 1)) && (n == 0 || wait_warp(bar_o, ph ^ 1u));
             if (!ok) break;
             ptx::tc_fence_after();
-            if (lane == 0) {
-#pragma unroll 4
-                for (int ks = 0; ks < DAB / 16; ++ks)
-                    ptx::mma_bf16(t_sc, kda::tc::kdesc(at, ks, kC), kda::tc::kdesc(bt, ks, kC), id_sc, ks > 0);
-                ptx::mma_commit(bar_sc);
-            }
-            __syncwarp();
+#pragma unroll
+            for (int ks = 0; ks < DAB / 16; ++ks)
+                ptx::mma_bf16_elected(me, u_sc, kda::tc::kdesc(at, ks, kC), kda::tc::kdesc(bt, ks, kC), id_sc, ks > 0);
+            ptx::mma_commit_elected(me, bar_sc);
             ok = wait_warp(bar_x, ph) && (n == 0 || wait_warp(bar_od, ph ^ 1u));
             if (!ok) break;
             ptx::tc_fence_after();
-            if (lane == 0) {
-#pragma unroll 4
-                for (int ks = 0; ks < DAB / 16; ++ks)
-                    ptx::mma_bf16(t_oi, kda::tc::kdesc(at, ks, kC),
-                                  ptx::desc_mnmajor_sw128(sb + L::X + ks * 2048, DAB * 128, 1024), id_in, ks > 0);
-                ptx::mma_commit(bar_in);
-            }
-            __syncwarp();
+#pragma unroll
+            for (int ks = 0; ks < DAB / 16; ++ks)
+                ptx::mma_bf16_elected(me, u_oi, kda::tc::kdesc(at, ks, kC),
+                                      ptx::desc_mnmajor_sw128(sbu + L::X + ks * 2048, DAB * 128, 1024), id_in, ks > 0);
+            ptx::mma_commit_elected(me, bar_in);
             if (!(ok = wait_warp(bar_b, ph))) break;
             ptx::tc_fence_after();
             if (it.need_u(want_last)) {
-                if (lane == 0) {
-                    const bool three = want_last && it.whole;
-                    auto term = [&](uint32_t x, uint32_t acc) {
-#pragma unroll 4
-                        for (int ks = 0; ks < kC / 16; ++ks)
-                            ptx::mma_bf16(t_u, ptx::desc_mnmajor_sw128(x + ks * 2048, 16384, 1024),
-                                          ptx::desc_mnmajor_sw128(ct + ks * 2048, 16384, 1024), id_u, acc + ks > 0);
-                    };
-                    // small terms first: the accumulator is least rounded while it is small
-                    if (three) term(sb + L::X, 0);
-                    term(at, three ? 1 : 0);
-                    term(bt, 1);
-                    ptx::mma_commit(bar_u);
+                const bool three = role.three && it.whole;
+                // small terms first: the accumulator is least rounded while it is small
+#pragma unroll 1
+                for (int x = three ? 0 : 1; x < 3; ++x) {
+                    const uint32_t term = __shfl_sync(0xffffffffu, x == 0 ? sbu + L::X : x == 1 ? at : bt, 0);
+                    const uint32_t acc = x > (three ? 0 : 1) ? 1u : 0u;
+#pragma unroll
+                    for (int ks = 0; ks < kC / 16; ++ks)
+                        ptx::mma_bf16_elected(me, u_u, ptx::desc_mnmajor_sw128(term + ks * 2048, 16384, 1024),
+                                              ptx::desc_mnmajor_sw128(ct + ks * 2048, 16384, 1024), id_u,
+                                              ks > 0 ? 1u : acc);
                 }
-                __syncwarp();
+                ptx::mma_commit_elected(me, bar_u);
             }
             if (!(ok = wait_warp(bar_p, ph))) break;
             ptx::tc_fence_after();
-            if (lane == 0) {
-#pragma unroll 4
-                for (int ks = 0; ks < kC / 16; ++ks)
-                    ptx::mma_bf16_ts(t_oa, t_sc + ks * 8, ptx::desc_mnmajor_sw128(ct + ks * 2048, 16384, 1024), id_in,
-                                     ks > 0);
-                ptx::mma_commit(bar_o);
-                ptx::mma_commit(bar_free + 8 * s);
-            }
-            __syncwarp();
+#pragma unroll
+            for (int ks = 0; ks < kC / 16; ++ks)
+                ptx::mma_bf16_ts_elected(me, u_oa, u_sc + ks * 8, ptx::desc_mnmajor_sw128(ct + ks * 2048, 16384, 1024),
+                                         id_in, ks > 0);
+            ptx::mma_commit_elected(me, bar_o);
+            ptx::mma_commit_elected(me, bar_free + 8 * s);
             ++n;
         }
         if (lane == 0) {   // products in flight
@@ -621,47 +679,50 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
             }
             if (!(ok = wait_out(bar_sc, ph))) break;
             ptx::tc_fence_after();
-            // 16 score columns a step (P overwrites scores that were read).  Loops over columns stay
+            // 32 score columns a step (P overwrites scores that were read).  The loops over columns stay
             // rolled here: the kernel's steady state has to fit the instruction cache.
-            const int open0 = dir > 0 ? 0 : 2 * quad + 2, open1 = dir > 0 ? 2 * quad : len >> 4;   // no row of the warp masked
 #pragma unroll 1
-            for (int b = 0; b < 8; ++b) {
-                uint32_t p[8];
-                if (b >= open0 && b < open1) {
-                    float s[16];
-                    ptx::tmem_ld16(t_sc + tl + 16 * b, s);
-                    const float r = kda::tc::exp2_fast(l2 * (dir > 0 ? i - 16 * b - 15 : 16 * b - i));
-                    ptx::tmem_wait_ld();
+            for (int b = 0; b < 4; ++b) {
+                uint32_t p[16];
+                if (dir > 0 ? b > quad : b < quad) {
 #pragma unroll
-                    for (int m = 0; m < 16; m += 2) {
-                        const float2 c = ptx::mul2(make_float2(step[m], step[m + 1]), make_float2(r, r));
-                        const float2 z = ptx::mul2(make_float2(s[m], s[m + 1]), c);
-                        p[m / 2] = pack2(z.x, z.y);
-                    }
-                } else if (dir > 0 ? b > 2 * quad + 1 : b < 2 * quad) {
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) p[x] = 0u;
+                    for (int x = 0; x < 16; ++x) p[x] = 0u;
                 } else {
-                    float s[16];
-                    ptx::tmem_ld16(t_sc + tl + 16 * b, s);
-                    // scores on the masked side and behind the end may be anything, and count as zeros
-                    const int side = (bi - b) * dir;   // 0: the row's own block, below: masked
-                    const int first = side == 0 && dir < 0 ? li : 0;
-                    const int last = side < 0 ? -1 : min(side == 0 && dir > 0 ? li : 15, len - 1 - 16 * b);
-                    const float r = kda::tc::exp2_fast(l2 * max(dir > 0 ? i - 16 * b - 15 : 16 * b - i, 0));
-                    ptx::tmem_wait_ld();
+                    float s[32];
+                    ptx::tmem_ld32(t_sc + tl + 32 * b, s);
+                    float r[2];
 #pragma unroll
-                    for (int m = 0; m < 16; m += 2) {
-                        float c[2], z[2];
+                    for (int k = 0; k < 2; ++k)
+                        r[k] = kda::tc::exp2_fast(l2 * max(dir > 0 ? i - 32 * b - 16 * k - 15 : 32 * b + 16 * k - i, 0));
+                    ptx::tmem_wait_ld();
+                    if (b != quad && (dir > 0 || 32 * b + 32 <= len)) {   // no row of the warp is masked
+#pragma unroll
+                        for (int m = 0; m < 32; m += 2) {
+                            const float2 c = ptx::mul2(make_float2(step[m & 15], step[(m & 15) + 1]), make_float2(r[m >> 4], r[m >> 4]));
+                            const float2 z = ptx::mul2(make_float2(s[m], s[m + 1]), c);
+                            p[m / 2] = pack2(z.x, z.y);
+                        }
+                    } else {
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            c[k] = side == 0 ? near[m + k] : step[m + k] * r;
-                            z[k] = m + k >= first && m + k <= last ? s[m + k] * c[k] : 0.f;
+                            // scores on the masked side and behind the end may be anything, and count as zeros
+                            const int side = (bi - 2 * b - k) * dir;   // 0: the row's own block, below: masked
+                            const int first = side == 0 && dir < 0 ? li : 0;
+                            const int last = side < 0 ? -1 : min(side == 0 && dir > 0 ? li : 15, len - 1 - 32 * b - 16 * k);
+#pragma unroll
+                            for (int m = 0; m < 16; m += 2) {
+                                float z[2];
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const float c = side == 0 ? near[m + e] : step[m + e] * r[k];
+                                    z[e] = m + e >= first && m + e <= last ? s[16 * k + m + e] * c : 0.f;
+                                }
+                                p[8 * k + m / 2] = pack2(z[0], z[1]);
+                            }
                         }
-                        p[m / 2] = pack2(z[0], z[1]);
                     }
                 }
-                ptx::tmem_st8(t_sc + tl + 8 * b, p);
+                ptx::tmem_st16(t_sc + tl + 16 * b, p);
             }
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
@@ -696,24 +757,15 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar_od);
-            if (quad * 32 + 32 <= len) {
-                if (lane == 0) {
-#pragma unroll
-                    for (int a = 0; a < DC / 64; ++a)
-                        ptx::tma_store_3d(&role.out_map, tile + a * 16384 + quad * 4096, a * 64, h,
-                                          (int)t + quad * 32);
-                    ptx::bulk_commit();
-                    ptx::bulk_wait_read_all();
-                }
-            } else {   // a sequence ends in these rows: the ones behind it are not this sequence's
-                for (int x = lane; x < 32 * (DC / 8); x += 32) {
-                    const int r = quad * 32 + x / (DC / 8), cg = x % (DC / 8);
+            if (quad * kOutBox + kOutBox > len) {   // a sequence ends in these rows
+                for (int x = lane; x < kOutBox * (DC / 8); x += 32) {
+                    const int r = quad * kOutBox + x / (DC / 8), cg = x % (DC / 8);
                     if (r < len)
                         *reinterpret_cast<uint4 *>(role.out + ((t + r) * g.H + h) * DC + cg * 8) =
                             ptx::lds128(tile + (cg >> 3) * 16384 + swz(r, cg & 7));
                 }
+                __syncwarp();
             }
-            __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar_out + 8 * s);
             ++n;
         }
@@ -738,7 +790,7 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
                 head = h;
                 wlen = len;
                 const float lg = log_decay[h];
-                wt = Weight(r < len ? (float)exp((double)lg * (dir > 0 ? len - 1 - r : r + 1)) : 0.f);
+                wt = Weight(r < len ? (float)exp64((double)lg * (dir > 0 ? len - 1 - r : r + 1)) : 0.f);
                 dec = decay2(lg, len);
             }
             if (it.first) {
@@ -785,31 +837,55 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
                     ptx::sts128(ct + (cg >> 3) * 16384 + swz(r, cg & 7), 0, 0, 0, 0);
                 }
             }
-            // inter done: scores are taken too, the tiles of A and X are free
+            const bool need = it.need_u(want_last), three = role.three && it.whole;
+            auto group_at = [&](int k) {
+                const int cg = part * BG + k;
+                return (uint32_t)((cg >> 3) * 16384 + swz(r, cg & 7));
+            };
+            // two terms: the leading one takes b's place once the scores are done; the second waits in
+            // registers for the tile of A
+            constexpr int EG = BG / 2;
+            uint4 mid[EG];
+            if (need && !three) {
+                if (!(ok = wait_state(bar_sc, ph))) break;
+#pragma unroll
+                for (int k = 0; k < EG; ++k) {
+                    uint4 t0, t2, x = ptx::lds128(bt + group_at(k));
+                    if (r >= len) x = make_uint4(0, 0, 0, 0);
+                    split8<false>(x, wt, t0, mid[k], t2);
+                    ptx::sts128(bt + group_at(k), t0);
+                }
+            }
+            // inter done: the tiles of A and X are free
             if (!(ok = wait_state(bar_in, ph))) break;
-            const bool need = it.need_u(want_last);
-            if (need) {
-                const bool three = want_last && it.whole;
-                // four groups a step: their loads in flight together, and a body that fits the instruction cache
+            if (need && !three) {
+#pragma unroll
+                for (int k = 0; k < EG; ++k) ptx::sts128(at + group_at(k), mid[k]);
+#pragma unroll
+                for (int k = EG; k < BG; ++k) mid[k - EG] = ptx::lds128(bt + group_at(k));
+#pragma unroll
+                for (int k = EG; k < BG; ++k) {
+                    uint4 t0, t1, t2, x = mid[k - EG];
+                    if (r >= len) x = make_uint4(0, 0, 0, 0);
+                    split8<false>(x, wt, t0, t1, t2);
+                    ptx::sts128(bt + group_at(k), t0);
+                    ptx::sts128(at + group_at(k), t1);
+                }
+            } else if (need) {
+                // two groups a step: their loads in flight together, and a body that fits the instruction cache
 #pragma unroll 1
-                for (int k = 0; k < BG; k += 4) {
-                    uint4 x[4];
-                    uint32_t off[4];
+                for (int k = 0; k < BG; k += 2) {
+                    uint4 x[2];
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const int cg = part * BG + k + z;
-                        off[z] = (cg >> 3) * 16384 + swz(r, cg & 7);
-                        x[z] = ptx::lds128(bt + off[z]);
-                    }
+                    for (int z = 0; z < 2; ++z) x[z] = ptx::lds128(bt + group_at(k + z));
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) {
+                    for (int z = 0; z < 2; ++z) {
                         uint4 t0, t1, t2;
                         if (r >= len) x[z] = make_uint4(0, 0, 0, 0);
-                        if (three) split8<true>(x[z], wt, t0, t1, t2);
-                        else split8<false>(x[z], wt, t0, t1, t2);
-                        ptx::sts128(bt + off[z], t0);
-                        ptx::sts128(at + off[z], t1);
-                        if (three) ptx::sts128(sb + L::X + off[z], t2);
+                        split8<true>(x[z], wt, t0, t1, t2);
+                        ptx::sts128(bt + group_at(k + z), t0);
+                        ptx::sts128(at + group_at(k + z), t1);
+                        ptx::sts128(sb + L::X + group_at(k + z), t2);
                     }
                 }
             }
@@ -822,13 +898,13 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
                 ptx::tc_fence_after();
                 if (quad * 32 < DAB) {
 #pragma unroll
-                    for (int b = 0; b < CPT / 32; ++b) {
-                        float v[32];
-                        ptx::tmem_ld32(t_u + tl + 32 * b, v);
+                    for (int b = 0; b < CPT / 16; ++b) {
+                        float v[16];
+                        ptx::tmem_ld16(t_u + tl + 16 * b, v);
                         ptx::tmem_wait_ld();
 #pragma unroll
-                        for (int x = 0; x < 32; x += 2) {
-                            float *z = S + 32 * b + x;
+                        for (int x = 0; x < 16; x += 2) {
+                            float *z = S + 16 * b + x;
                             const float2 o = make_float2(z[0], z[1]);
                             const float2 n2 = ptx::fma2(make_float2(dec.x, dec.x), o,
                                                         ptx::fma2(make_float2(dec.y, dec.y), o, make_float2(v[x], v[x + 1])));
@@ -908,14 +984,14 @@ cudaError_t tc_forward(const Call &c, const void *q, const void *k, const void *
     cudaError_t e;
     if (cuts<kC>(g)) {
         SumArgs a{};
-        a.role[0] = SumRole{tk, tv, y.sum_in, y.sum_out, 1, last != nullptr};
+        a.role[0] = SumRole{tk, tv, y.sum_in, y.sum_out, 1, 1, last != nullptr};
         if ((e = launch_sum<DK, DV>(g, a, 1, c)) != cudaSuccess) return e;
         if ((e = launch_join<kC, 1, true>(g, y, c, DK * DV)) != cudaSuccess) return e;
     } else if ((e = launch_empty<kC>(g, y, c, DK * DV)) != cudaSuccess) {
         return e;
     }
     WalkArgs a{};
-    a.role[0] = WalkRole{tq, tk, tv, to, (__nv_bfloat16 *)o, y, 1, 0};
+    a.role[0] = WalkRole{tq, tk, tv, to, (__nv_bfloat16 *)o, y, 1, 1, 0};
     return launch_walk<DK, DV>(g, a, 1, c);
 }
 
@@ -935,8 +1011,8 @@ cudaError_t tc_backward(const Call &c, const void *q, const void *k, const void 
     cudaError_t e;
     if (cuts<kC>(g)) {
         SumArgs a{};
-        a.role[0] = SumRole{tk, tv, fwd.sum_in, fwd.sum_out, 1, 0};
-        a.role[1] = SumRole{tq, td, bwd.sum_in, bwd.sum_out, -1, dinit != nullptr};
+        a.role[0] = SumRole{tk, tv, fwd.sum_in, fwd.sum_out, 1, 0, 0};
+        a.role[1] = SumRole{tq, td, bwd.sum_in, bwd.sum_out, -1, 1, dinit != nullptr};
         if ((e = launch_sum<DK, DV>(g, a, 2, c)) != cudaSuccess) return e;
         if ((e = launch_join<kC, 1, true>(g, fwd, c, E)) != cudaSuccess) return e;
         if ((e = launch_join<kC, -1, true>(g, bwd, c, E)) != cudaSuccess) return e;
@@ -945,8 +1021,8 @@ cudaError_t tc_backward(const Call &c, const void *q, const void *k, const void 
     }
     Carry bwd_t = bwd;
     bwd_t.last = nullptr;
-    const WalkRole r_dq{td, tv, tk, odq, (__nv_bfloat16 *)dq, fwd, 1, 1}, r_dk{tv, td, tq, odk, (__nv_bfloat16 *)dk, bwd_t, -1, 1},
-        r_dv{tk, tq, td, odv, (__nv_bfloat16 *)dv, bwd, -1, 0};
+    const WalkRole r_dq{td, tv, tk, odq, (__nv_bfloat16 *)dq, fwd, 1, 0, 1}, r_dk{tv, td, tq, odk, (__nv_bfloat16 *)dk, bwd_t, -1, 0, 1},
+        r_dv{tk, tq, td, odv, (__nv_bfloat16 *)dv, bwd, -1, 1, 0};
     WalkArgs a{};
     a.role[0] = r_dq;
     a.role[1] = r_dk;
