@@ -13,9 +13,9 @@ OBJ = os.path.join(HERE, "build")
 UNITS = {
     "kda_lib.cu": ["kda_common.cuh", "kda_decode.cuh", "kda_chunk_simt.cuh", "kda_chunk_tc.cuh", "kda_chunk_2pass.cuh",
                    "kda_bwd_simt.cuh", "kda_bwd_tc.cuh", "tc_ptx.cuh", "tc_tile.cuh", "kda_host.h"],
-    "kda_la_lib.cu": ["kda_common.cuh", "kda_la.cuh", "kda_la_simt.cuh", "kda_la_tc.cuh", "kda_la_step.cuh", "tc_ptx.cuh",
-                      "tc_tile.cuh", "kda_host.h"],
-    "kda_norm_lib.cu": ["kda_common.cuh", "kda_norm.cuh", "tc_ptx.cuh", "kda_host.h"],
+    "kda_la_lib.cu": ["kda_common.cuh", "kda_la.cuh", "kda_la_simt.cuh", "kda_la_tc.cuh", "kda_la_step.cuh", "kda_launch.cuh",
+                      "tc_ptx.cuh", "tc_tile.cuh", "kda_host.h"],
+    "kda_norm_lib.cu": ["kda_common.cuh", "kda_launch.cuh", "kda_norm.cuh", "tc_ptx.cuh", "kda_host.h"],
 }
 
 NVCC_FLAGS = [

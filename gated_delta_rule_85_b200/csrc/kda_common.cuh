@@ -15,6 +15,13 @@ static __device__ unsigned int g_status;
 
 __device__ __forceinline__ void flag_status(unsigned int bits) { atomicOr(&g_status, bits); }
 
+// Kernels of one call follow each other by programmatic dependent launch (kda_launch.cuh): the next
+// one's CTAs may start while this one runs, and wait here for all of it (and, as it waited too,
+// for all before it).  Every thread of a kernel that is launched so calls this before it reads what
+// an earlier kernel of the call wrote, writes anything, or exits.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ----------------------------------------------------------------- input access
 
 template <typename T>

@@ -135,87 +135,128 @@ struct Carry {
     float *last;         // final states [rows][H][dk dv] or null
 };
 
-// Joins the cut parts: thread = four elements of the state; CTA column w (blockIdx.x < W)
-// follows the sequence that goes on behind span w from span to span.  The sums are
-// independent loads, fetched kAhead spans ahead of the recurrence that adds them up, and the
-// decays of 32 spans at a time are one warp's work (fp64 exponentials by every thread took
-// longer than the loads: 14 us of a 196 us prefill).
-// WANT_LAST: the part in the span where the sequence ends has a sum too, and `last` is
-// written here; without it the walk writes it.  Columns W.. (packed): one sequence each,
-// handed through when it has no tokens.
-template <int C, int DIR, bool WANT_LAST>
-__global__ void __launch_bounds__(256) la_join_kernel(Geo g, Carry y, const float *__restrict__ log_decay, int E,
+// Joins the cut parts of up to two sets of carried states (blockIdx.z), each in its direction.
+// Thread = kJoinVecs x four elements of the state; CTA column w (blockIdx.x < W) follows the
+// sequence that goes on behind span w from span to span.  The sums are independent loads,
+// fetched kAhead spans ahead of the recurrence that adds them up, and the decays of 32 spans at
+// a time are one warp's work (fp64 exponentials by every thread took longer than the loads).
+// finals: the part in the span where the sequence ends has a sum too, and `last` is written
+// here; without it the walk writes it.  Columns W.. (packed): one sequence each, handed
+// through when it has no tokens.
+constexpr int kJoinVecs = 2;
+struct Join {
+    Carry y;
+    int dir;
+    int finals;
+};
+struct Joins {
+    Join j[2];
+};
+template <int C>
+__global__ void __launch_bounds__(256) la_join_kernel(Geo g, const __grid_constant__ Joins joins,
+                                                      const float *__restrict__ log_decay, int E,
                                                       const int32_t *__restrict__ slots, int num_slots) {
-    const int e = (blockIdx.y * 256 + threadIdx.x) * 4;   // E is a multiple of 1024
-    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    let_next_start();
+    const Join &job = joins.j[blockIdx.z];
+    const Carry &y = job.y;
+    const int dir = job.dir;
+    const int e0 = (blockIdx.y * 256 * kJoinVecs + threadIdx.x) * 4;   // and every 1024 on; E is a multiple of 1024 kJoinVecs
+    struct V {
+        float4 v[kJoinVecs];
+    };
+    auto load = [&](const float *p) {
+        V r;
+#pragma unroll
+        for (int k = 0; k < kJoinVecs; ++k) r.v[k] = load4(p + e0 + k * 1024);
+        return r;
+    };
+    auto store = [&](float *p, const V &x) {
+#pragma unroll
+        for (int k = 0; k < kJoinVecs; ++k) store4(p + e0 + k * 1024, x.v[k]);
+    };
+    V zero;
+#pragma unroll
+    for (int k = 0; k < kJoinVecs; ++k) zero.v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     if ((int)blockIdx.x >= g.W) {
         const int n = blockIdx.x - g.W;
         long long t0, t1;
         seq_span(g.cu, g.T, n, t0, t1);
         const int row = state_row(slots, num_slots, n);
+        wait_for_previous();
         if (t1 > t0 || !y.last || y.last == y.s0 || row < 0) return;
         for (int h = 0; h < g.H; ++h) {
-            const long long off = ((long long)row * g.H + h) * E + e;
-            store4(y.last + off, y.s0 ? load4(y.s0 + off) : zero);
+            const long long off = ((long long)row * g.H + h) * E;
+            store(y.last + off, y.s0 ? load(y.s0 + off) : zero);
         }
         return;
     }
-    int w = blockIdx.x;
-    const long long lo = g.lo(w), hi = g.hi(w);
+    const int w0 = blockIdx.x;
+    const long long lo = g.lo(w0), hi = g.hi(w0);
     Cursor<C> cur;
-    const long long edge = DIR > 0 ? hi - 1 : lo;
+    const long long edge = dir > 0 ? hi - 1 : lo;
     cur.seek(g, edge);
     // the sequence at the span's far edge must start inside the span and go on behind it
-    if (!cur.valid || cur.c == (DIR > 0 ? cur.nck - 1 : 0)) return;
-    const long long u_first = DIR > 0 ? edge - cur.c : edge + (cur.nck - 1 - cur.c);
-    if (DIR > 0 ? u_first < lo : u_first >= hi) return;
-    const long long u_last = DIR > 0 ? u_first + cur.nck - 1 : u_first - (cur.nck - 1);
+    const long long u_first = dir > 0 ? edge - cur.c : edge + (cur.nck - 1 - cur.c);
+    const bool mine = cur.valid && cur.c != (dir > 0 ? cur.nck - 1 : 0) && (dir > 0 ? u_first >= lo : u_first < hi);
+    if (!mine) {
+        wait_for_previous();
+        return;
+    }
+    const long long u_last = dir > 0 ? u_first + cur.nck - 1 : u_first - (cur.nck - 1);
     const int row = state_row(slots, num_slots, cur.n);
-    const long long off = ((long long)max(row, 0) * g.H + cur.h) * E + e;
-    const float4 s0 = row >= 0 && y.s0 ? load4(y.s0 + off) : zero;
-    const float4 out0 = load4(y.sum_out + (long long)w * E + e);
-    if (y.s0_copy) store4(y.s0_copy + ((long long)cur.n * g.H + cur.h) * E + e, s0);
-    auto add = [](float2 d, float4 s, float4 u) {
-        return make_float4(fmaf(d.x, s.x, fmaf(d.y, s.x, u.x)), fmaf(d.x, s.y, fmaf(d.y, s.y, u.y)),
-                           fmaf(d.x, s.z, fmaf(d.y, s.z, u.z)), fmaf(d.x, s.w, fmaf(d.y, s.w, u.w)));
-    };
-    // spans behind w that the sequence crosses from edge to edge; in the next one it ends
-    auto crossed = [&](int x) { return x >= 0 && x < g.W && (DIR > 0 ? u_last >= g.hi(x) : u_last < g.lo(x)); };
-    const int w0 = w;
+    const long long off = ((long long)max(row, 0) * g.H + cur.h) * E;
+    // spans behind w0 that the sequence crosses from edge to edge; in the next one it ends
+    auto crossed = [&](int x) { return x >= 0 && x < g.W && (dir > 0 ? u_last >= g.hi(x) : u_last < g.lo(x)); };
     // tokens of the sequence in span x
     auto tokens = [&](int x) -> double {
-        if (x == w0) return DIR > 0 ? (double)(cur.c + 1) * C : (double)(cur.t1 - cur.tok());
+        if (x == w0) return dir > 0 ? (double)(cur.c + 1) * C : (double)(cur.t1 - cur.tok());
         if (crossed(x)) return (double)(g.hi(x) - g.lo(x)) * C;
-        return DIR > 0 ? (double)(cur.t1 - (cur.t0 + (g.lo(x) - u_first) * C)) : (double)(g.hi(x) - u_last) * C;
+        return dir > 0 ? (double)(cur.t1 - (cur.t0 + (g.lo(x) - u_first) * C)) : (double)(g.hi(x) - u_last) * C;
     };
     __shared__ float2 dec[32];   // of the spans from `base` on
     int base = 0;
     auto decays = [&]() {
         __syncthreads();
         if (threadIdx.x < 32) {
-            const int x = w0 + (base + (int)threadIdx.x) * DIR;
+            const int x = w0 + (base + (int)threadIdx.x) * dir;
             // behind the span where the sequence ends nothing is asked for
-            dec[threadIdx.x] = threadIdx.x + base > 0 && !crossed(x - DIR) && x - DIR != w0
+            dec[threadIdx.x] = threadIdx.x + base > 0 && !crossed(x - dir) && x - dir != w0
                                    ? make_float2(0.f, 0.f)
                                    : decay2(log_decay[cur.h], tokens(x));
         }
         __syncthreads();
     };
     decays();
-    float4 s = add(dec[0], s0, out0);
-    int i = 1;
-    w += DIR;
-    store4(y.start + (long long)w * E + e, s);
-    constexpr int kAhead = 8;
-    while (crossed(w)) {
-        float4 u[kAhead];
-        int m = 0;
+    auto add = [](float2 d, const V &s, const V &u) {
+        auto one = [&](float a, float b) { return fmaf(d.x, a, fmaf(d.y, a, b)); };
+        V r;
+#pragma unroll
+        for (int k = 0; k < kJoinVecs; ++k)
+            r.v[k] = make_float4(one(s.v[k].x, u.v[k].x), one(s.v[k].y, u.v[k].y), one(s.v[k].z, u.v[k].z),
+                                 one(s.v[k].w, u.v[k].w));
+        return r;
+    };
+    wait_for_previous();
+    const V s0 = row >= 0 && y.s0 ? load(y.s0 + off) : zero;
+    const V out0 = load(y.sum_out + (long long)w0 * E);
+    constexpr int kAhead = 4;
+    V u[kAhead];
+    int w = w0 + dir, m = 0;
+    auto fetch = [&]() {   // the sums of spans w.. that are crossed
+        m = 0;
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
-            if (m == k && crossed(w + k * DIR)) {
-                u[k] = load4(y.sum_in + (long long)(w + k * DIR) * E + e);
+            if (m == k && crossed(w + k * dir)) {
+                u[k] = load(y.sum_in + (long long)(w + k * dir) * E);
                 m = k + 1;
             }
+    };
+    fetch();
+    if (y.s0_copy) store(y.s0_copy + ((long long)cur.n * g.H + cur.h) * E, s0);
+    V s = add(dec[0], s0, out0);
+    int i = 1;
+    store(y.start + (long long)w * E, s);
+    while (m > 0) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
             if (k < m) {
@@ -225,16 +266,18 @@ __global__ void __launch_bounds__(256) la_join_kernel(Geo g, Carry y, const floa
                 }
                 s = add(dec[i - base], s, u[k]);
                 ++i;
-                w += DIR;
-                store4(y.start + (long long)w * E + e, s);
+                w += dir;
+                store(y.start + (long long)w * E, s);
             }
+        fetch();
     }
-    if (WANT_LAST && y.last && row >= 0) {
+    if (job.finals && y.last && row >= 0) {
+        const V end = load(y.sum_in + (long long)w * E);
         if (i - base == 32) {
             base = i;
             decays();
         }
-        store4(y.last + off, add(dec[i - base], s, load4(y.sum_in + (long long)w * E + e)));
+        store(y.last + off, add(dec[i - base], s, end));
     }
 }
 

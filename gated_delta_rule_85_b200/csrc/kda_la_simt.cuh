@@ -7,6 +7,7 @@
 #pragma once
 
 #include "kda_la.cuh"
+#include "kda_launch.cuh"
 
 namespace kda {
 namespace la {
@@ -50,6 +51,8 @@ __global__ void __launch_bounds__(256) la_simt_kernel(Geo g, Walk wk, const floa
                                                       const int32_t *__restrict__ slots, int num_slots) {
     using L = SimtSmem<DAB, DC>;
     constexpr int RM = DAB / 16, CG = DC / 64;   // state rows of a thread; its columns: 4 tx + 64 j
+    let_next_start();
+    wait_for_previous();
     extern __shared__ __align__(16) float sm[];
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int w = blockIdx.x;
@@ -302,11 +305,15 @@ inline Carry carry_at(float *ws, int W, int E) {
     return y;
 }
 
-template <int C, int DIR, bool WANT_LAST>
-cudaError_t launch_join(const Geo &g, const Carry &y, const Call &c, int E) {
-    const dim3 grid(g.W + (g.cu ? g.N : 0), E / 1024);
-    la_join_kernel<C, DIR, WANT_LAST><<<grid, 256, 0, c.st>>>(g, y, c.log_decay, E, c.slots, c.num_slots);
-    return cudaGetLastError();
+// One or two sets of carried states (directions `dirs`); the kernel in front of it wrote their sums.
+template <int C>
+cudaError_t launch_join(const Geo &g, const Call &c, int E, bool finals, const Carry &y, int dir,
+                        const Carry *y2 = nullptr) {
+    Joins j{};
+    j.j[0] = Join{y, dir, finals};
+    if (y2) j.j[1] = Join{*y2, -dir, finals};
+    const dim3 grid(g.W + (g.cu ? g.N : 0), E / (1024 * kJoinVecs), y2 ? 2 : 1);
+    return launch_after(la_join_kernel<C>, grid, 256, 0, c.st, g, j, c.log_decay, E, c.slots, c.num_slots);
 }
 
 // Where nothing is cut the join has only empty packed sequences' states to hand through.
@@ -315,15 +322,20 @@ cudaError_t launch_empty(const Geo &g, const Carry &y, const Call &c, int E) {
     if (!g.cu || !y.last || y.last == y.s0) return cudaSuccess;
     Geo none = g;
     none.W = 0;
-    return launch_join<C, 1, false>(none, y, c, E);
+    Joins j{};
+    j.j[0] = Join{y, 1, 0};
+    la_join_kernel<C><<<dim3(g.N, E / (1024 * kJoinVecs)), 256, 0, c.st>>>(none, j, c.log_decay, E, c.slots, c.num_slots);
+    return cudaGetLastError();
 }
 
+// after: behind another kernel of the call
 template <int DAB, int DC, typename Tin, int DIR, bool WALK>
-cudaError_t launch_simt(const Geo &g, const Walk &wk, const Call &c) {
+cudaError_t launch_simt(const Geo &g, const Walk &wk, const Call &c, bool after = true) {
     constexpr size_t smem = SimtSmem<DAB, DC>::bytes;
     auto kern = la_simt_kernel<DAB, DC, Tin, DIR, WALK>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
+    if (after) return launch_after(kern, g.W, 256, smem, c.st, g, wk, c.log_decay, c.slots, c.num_slots);
     kern<<<g.W, 256, smem, c.st>>>(g, wk, c.log_decay, c.slots, c.num_slots);
     return cudaGetLastError();
 }
@@ -339,13 +351,14 @@ cudaError_t simt_forward(const Call &c, const void *q, const void *k, const void
     // a pool is read and written by different CTAs of the walk: it reads cut sequences' states from a copy
     if (c.slots) wk.y.s0_copy = ws + (size_t)3 * g.W * DK * DV;
     cudaError_t e;
-    if (cuts<kSimtC>(g)) {
-        if ((e = launch_simt<DK, DV, Tin, 1, false>(g, wk, c)) != cudaSuccess) return e;
-        if ((e = launch_join<kSimtC, 1, false>(g, wk.y, c, DK * DV)) != cudaSuccess) return e;
+    const bool cut = cuts<kSimtC>(g);
+    if (cut) {
+        if ((e = launch_simt<DK, DV, Tin, 1, false>(g, wk, c, false)) != cudaSuccess) return e;
+        if ((e = launch_join<kSimtC>(g, c, DK * DV, false, wk.y, 1)) != cudaSuccess) return e;
     } else if ((e = launch_empty<kSimtC>(g, wk.y, c, DK * DV)) != cudaSuccess) {
         return e;
     }
-    return launch_simt<DK, DV, Tin, 1, true>(g, wk, c);
+    return launch_simt<DK, DV, Tin, 1, true>(g, wk, c, cut);
 }
 
 // Backward: dq walks forwards on S^T; dk and dv backwards on X, whose last state is dinit.
@@ -360,17 +373,17 @@ cudaError_t simt_backward(const Call &c, const void *q, const void *k, const voi
     bwd.last = dinit;
     const Walk sum_f{nullptr, k, v, nullptr, fwd, false}, sum_b{nullptr, q, d_o, nullptr, bwd, false};
     cudaError_t e;
-    if (cuts<kSimtC>(g)) {
-        if ((e = launch_simt<DK, DV, Tin, 1, false>(g, sum_f, c)) != cudaSuccess) return e;
+    const bool cut = cuts<kSimtC>(g);
+    if (cut) {
+        if ((e = launch_simt<DK, DV, Tin, 1, false>(g, sum_f, c, false)) != cudaSuccess) return e;
         if ((e = launch_simt<DK, DV, Tin, -1, false>(g, sum_b, c)) != cudaSuccess) return e;
-        if ((e = launch_join<kSimtC, 1, false>(g, fwd, c, E)) != cudaSuccess) return e;
-        if ((e = launch_join<kSimtC, -1, false>(g, bwd, c, E)) != cudaSuccess) return e;
+        if ((e = launch_join<kSimtC>(g, c, E, false, fwd, 1, &bwd)) != cudaSuccess) return e;
     } else if ((e = launch_empty<kSimtC>(g, bwd, c, E)) != cudaSuccess) {
         return e;
     }
     Carry bwd_t = bwd;
     bwd_t.last = nullptr;
-    if ((e = launch_simt<DV, DK, Tin, 1, true>(g, Walk{d_o, v, k, dq, fwd, true}, c)) != cudaSuccess) return e;
+    if ((e = launch_simt<DV, DK, Tin, 1, true>(g, Walk{d_o, v, k, dq, fwd, true}, c, cut)) != cudaSuccess) return e;
     if ((e = launch_simt<DV, DK, Tin, -1, true>(g, Walk{v, d_o, q, dk, bwd_t, true}, c)) != cudaSuccess) return e;
     return launch_simt<DK, DV, Tin, -1, true>(g, Walk{k, q, d_o, dv, bwd, false}, c);
 }

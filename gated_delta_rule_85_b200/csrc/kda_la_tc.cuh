@@ -20,6 +20,7 @@
 #include <type_traits>
 
 #include "kda_la.cuh"
+#include "kda_launch.cuh"
 #include "tc_ptx.cuh"
 #include "tc_tile.cuh"
 
@@ -154,6 +155,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
 la_sum_kernel(const __grid_constant__ SumArgs args, Geo g, const float *__restrict__ log_decay) {
     using L = SumSmem<DB, DC>;
     constexpr int NST = L::NST;
+    let_next_start();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sb = ptx::smem_u32(sm);
@@ -487,6 +489,7 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
                const int32_t *__restrict__ slots, int num_slots, int roles) {
     using L = WalkSmem<DAB, DC>;
     constexpr int NST = L::NST;
+    let_next_start();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sb = ptx::smem_u32(sm);
@@ -530,6 +533,7 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
     SpanWalk it(g, w, dir);
     bool ok = true;
     int n = 0;   // chunks so far
+    wait_for_previous();
 
     if (warp == 0) {
         // ---------------- producer, and the sender of outputs
@@ -958,12 +962,15 @@ cudaError_t launch_sum(const Geo &g, const SumArgs &a, int roles, const Call &c)
     return cudaGetLastError();
 }
 
+// after: behind another kernel of the call
 template <int DAB, int DC>
-cudaError_t launch_walk(const Geo &g, const WalkArgs &a, int roles, const Call &c) {
+cudaError_t launch_walk(const Geo &g, const WalkArgs &a, int roles, const Call &c, bool after) {
     constexpr int smem = WalkSmem<DAB, DC>::ALLOC;
     auto kern = la_walk_kernel<DAB, DC>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    if (after)
+        return launch_after(kern, g.W * roles, kWalkThreads, smem, c.st, a, g, c.log_decay, c.slots, c.num_slots, roles);
     kern<<<g.W * roles, kWalkThreads, smem, c.st>>>(a, g, c.log_decay, c.slots, c.num_slots, roles);
     return cudaGetLastError();
 }
@@ -982,17 +989,18 @@ cudaError_t tc_forward(const Call &c, const void *q, const void *k, const void *
     // a pool is read and written by different CTAs of the walk: it reads cut sequences' states from a copy
     if (c.slots) y.s0_copy = ws + (size_t)3 * g.W * DK * DV;
     cudaError_t e;
-    if (cuts<kC>(g)) {
+    const bool cut = cuts<kC>(g);
+    if (cut) {
         SumArgs a{};
         a.role[0] = SumRole{tk, tv, y.sum_in, y.sum_out, 1, 1, last != nullptr};
         if ((e = launch_sum<DK, DV>(g, a, 1, c)) != cudaSuccess) return e;
-        if ((e = launch_join<kC, 1, true>(g, y, c, DK * DV)) != cudaSuccess) return e;
+        if ((e = launch_join<kC>(g, c, DK * DV, true, y, 1)) != cudaSuccess) return e;
     } else if ((e = launch_empty<kC>(g, y, c, DK * DV)) != cudaSuccess) {
         return e;
     }
     WalkArgs a{};
     a.role[0] = WalkRole{tq, tk, tv, to, (__nv_bfloat16 *)o, y, 1, 1, 0};
-    return launch_walk<DK, DV>(g, a, 1, c);
+    return launch_walk<DK, DV>(g, a, 1, c, cut);
 }
 
 template <int DK, int DV>
@@ -1009,13 +1017,13 @@ cudaError_t tc_backward(const Call &c, const void *q, const void *k, const void 
     bwd.s0 = dlast;
     bwd.last = dinit;
     cudaError_t e;
-    if (cuts<kC>(g)) {
+    const bool cut = cuts<kC>(g);
+    if (cut) {
         SumArgs a{};
         a.role[0] = SumRole{tk, tv, fwd.sum_in, fwd.sum_out, 1, 0, 0};
         a.role[1] = SumRole{tq, td, bwd.sum_in, bwd.sum_out, -1, 1, dinit != nullptr};
         if ((e = launch_sum<DK, DV>(g, a, 2, c)) != cudaSuccess) return e;
-        if ((e = launch_join<kC, 1, true>(g, fwd, c, E)) != cudaSuccess) return e;
-        if ((e = launch_join<kC, -1, true>(g, bwd, c, E)) != cudaSuccess) return e;
+        if ((e = launch_join<kC>(g, c, E, true, fwd, 1, &bwd)) != cudaSuccess) return e;
     } else if ((e = launch_empty<kC>(g, bwd, c, E)) != cudaSuccess) {
         return e;
     }
@@ -1028,11 +1036,11 @@ cudaError_t tc_backward(const Call &c, const void *q, const void *k, const void 
     a.role[1] = r_dk;
     if (DK == DV) {   // one launch: the three walks of a span share tiles
         a.role[2] = r_dv;
-        return launch_walk<DK, DV>(g, a, 3, c);
+        return launch_walk<DK, DV>(g, a, 3, c, cut);
     }
-    if ((e = launch_walk<DV, DK>(g, a, 2, c)) != cudaSuccess) return e;
+    if ((e = launch_walk<DV, DK>(g, a, 2, c, cut)) != cudaSuccess) return e;
     a.role[0] = r_dv;
-    return launch_walk<DK, DV>(g, a, 1, c);
+    return launch_walk<DK, DV>(g, a, 1, c, true);
 }
 
 }  // namespace la

@@ -16,6 +16,7 @@
 #include <algorithm>
 
 #include "kda_common.cuh"
+#include "kda_launch.cuh"
 #include "tc_ptx.cuh"
 
 namespace kda {
@@ -296,6 +297,7 @@ rows_backward_kernel(RowsGeo r, const T *__restrict__ dy, const T *__restrict__ 
                      const float *__restrict__ rstd, const float *__restrict__ weight,
                      const float *__restrict__ bias, const T *__restrict__ gate, T *__restrict__ dx,
                      T *__restrict__ dgate, float *__restrict__ part) {
+    let_next_start();
     constexpr int U = NV == 1 ? 2 : 1, P = vec_of<T>() / 2;
     using Raw = typename Vec<T, vec_of<T>()>::Raw;
     const Lane<T, NV, LANES> l(r, weight, bias);
@@ -460,6 +462,7 @@ __device__ __forceinline__ float2 pooled_moments(int lanes, float inv_count, Eac
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads) pos_moments_kernel(PosGeo p, const T *__restrict__ x,
                                                                float2 *__restrict__ part) {
+    let_next_start();
     __shared__ float sm_m[VEC * kThreads], sm_q[VEC * kThreads];
     const int tile = blockIdx.x % p.tiles, n = blockIdx.x / p.tiles, z = blockIdx.y;
     const int rl = threadIdx.x / p.tpr, cl = threadIdx.x % p.tpr, rows = kThreads / p.tpr;
@@ -533,6 +536,7 @@ __global__ void __launch_bounds__(kThreads) pos_apply_kernel(PosGeo p, const T *
                                                              const float2 *__restrict__ part,
                                                              float *__restrict__ mean, float *__restrict__ rstd,
                                                              float eps) {
+    wait_for_previous();
     __shared__ float2 stat[VEC * kThreads];   // (mean, rstd) of the block's groups
     const int tile = blockIdx.x % p.tiles, n = blockIdx.x / p.tiles, z = blockIdx.y;
     const Block<VEC> b(p, z);
@@ -623,6 +627,7 @@ __global__ void __launch_bounds__(kThreads) pos_back_sums_kernel(
     PosGeo p, const T *__restrict__ dy, const T *__restrict__ x, const float *__restrict__ mean,
     const float *__restrict__ rstd, const float *__restrict__ weight, const float *__restrict__ bias,
     const T *__restrict__ gate, T *__restrict__ dgate, float2 *__restrict__ chan, float2 *__restrict__ part) {
+    let_next_start();
     __shared__ float sm_w[VEC * kThreads], sm_b[VEC * kThreads];
     const int tile = blockIdx.x % p.tiles, n = blockIdx.x / p.tiles, z = blockIdx.y;
     const int rl = threadIdx.x / p.tpr, cl = threadIdx.x % p.tpr, rows = kThreads / p.tpr;
@@ -703,6 +708,7 @@ __global__ void __launch_bounds__(kThreads) pos_back_apply_kernel(
     const float *__restrict__ rstd, const float *__restrict__ weight, const float *__restrict__ bias,
     const T *__restrict__ gate, T *__restrict__ dx, const float2 *__restrict__ chan, const float2 *__restrict__ part,
     float *__restrict__ dweight, float *__restrict__ dbias) {
+    wait_for_previous();
     __shared__ float2 stat[VEC * kThreads];   // (m1, m2) of the block's groups
     const int lane = threadIdx.x & 31;
     if ((int)blockIdx.x >= p.N * p.tiles) {
@@ -788,6 +794,7 @@ __global__ void __launch_bounds__(kThreads) pos_back_apply_kernel(
 // channels a CTA, 32 warps over the partial sums.
 __global__ void __launch_bounds__(1024) rows_back_join_kernel(const float *__restrict__ part, int reps, long long C,
                                                               float *__restrict__ dweight, float *__restrict__ dbias) {
+    wait_for_previous();
     __shared__ float s[32][33];
     const int lane = threadIdx.x & 31, wp = threadIdx.x / 32;
     const long long c = (long long)blockIdx.x * 32 + lane;
@@ -903,13 +910,15 @@ cudaError_t launch_forward(const Plan &s, const Args &a, cudaStream_t st) {
     }
     const dim3 grid((unsigned)((long long)s.p.N * s.p.tiles), s.p.Z);
     float2 *part = (float2 *)a.ws;
-#define KDA_POS(VEC)                                                                                      \
-    pos_moments_kernel<T, VEC><<<grid, kThreads, 0, st>>>(s.p, x, part);                                  \
-    pos_apply_kernel<T, VEC, ACT, GATE><<<grid, kThreads, 0, st>>>(s.p, x, a.weight, a.bias, gate, y, part, \
-                                                                   a.mean, a.rstd, a.eps)
-    if (s.vec) { KDA_POS(VW); } else { KDA_POS(1); }
-#undef KDA_POS
-    return cudaGetLastError();
+    auto run = [&](auto moments, auto apply) {
+        moments<<<grid, kThreads, 0, st>>>(s.p, x, part);
+        const cudaError_t e = cudaGetLastError();
+        return e != cudaSuccess ? e
+                                : launch_after(apply, grid, kThreads, 0, st, s.p, x, a.weight, a.bias, gate, y, part,
+                                               a.mean, a.rstd, a.eps);
+    };
+    if (s.vec) return run(pos_moments_kernel<T, VW>, pos_apply_kernel<T, VW, ACT, GATE>);
+    return run(pos_moments_kernel<T, 1>, pos_apply_kernel<T, 1, ACT, GATE>);
 }
 
 template <typename T, int ACT, bool GATE>
@@ -926,22 +935,23 @@ cudaError_t launch_backward(const Plan &s, const Args &a, cudaStream_t st) {
         KDA_ROWS_CASES
 #undef KDA_ROWS
         if (a.dweight || a.dbias)
-            rows_back_join_kernel<<<dim3((unsigned)((C + 31) / 32), 2), 1024, 0, st>>>(part, s.r.step / s.r.G, C,
-                                                                                       a.dweight, a.dbias);
+            return launch_after(rows_back_join_kernel, dim3((unsigned)((C + 31) / 32), 2), 1024, 0, st, part,
+                                s.r.step / s.r.G, C, a.dweight, a.dbias);
         return cudaGetLastError();
     }
     const long long tiles = (long long)s.p.N * s.p.tiles;
     const dim3 grid((unsigned)tiles, s.p.Z);
     const unsigned join = a.dweight || a.dbias ? (s.p.C + 31) / 32 : 0;
     float2 *part = (float2 *)a.ws, *chan = part + (size_t)s.p.N * s.p.G * s.p.tiles * s.p.Z;
-#define KDA_POS(VEC)                                                                                              \
-    pos_back_sums_kernel<T, VEC, ACT, GATE><<<grid, kThreads, 0, st>>>(s.p, dy, x, a.mean, a.rstd, a.weight, a.bias, \
-                                                                       gate, dgate, chan, part);                  \
-    pos_back_apply_kernel<T, VEC, ACT, GATE><<<dim3(grid.x + join, grid.y), kThreads, 0, st>>>(                   \
-        s.p, dy, x, a.mean, a.rstd, a.weight, a.bias, gate, dx, chan, part, a.dweight, a.dbias)
-    if (s.vec) { KDA_POS(VW); } else { KDA_POS(1); }
-#undef KDA_POS
-    return cudaGetLastError();
+    auto run = [&](auto sums, auto apply) {
+        sums<<<grid, kThreads, 0, st>>>(s.p, dy, x, a.mean, a.rstd, a.weight, a.bias, gate, dgate, chan, part);
+        const cudaError_t e = cudaGetLastError();
+        return e != cudaSuccess ? e
+                                : launch_after(apply, dim3(grid.x + join, grid.y), kThreads, 0, st, s.p, dy, x, a.mean,
+                                               a.rstd, a.weight, a.bias, gate, dx, chan, part, a.dweight, a.dbias);
+    };
+    if (s.vec) return run(pos_back_sums_kernel<T, VW, ACT, GATE>, pos_back_apply_kernel<T, VW, ACT, GATE>);
+    return run(pos_back_sums_kernel<T, 1, ACT, GATE>, pos_back_apply_kernel<T, 1, ACT, GATE>);
 }
 
 template <typename T>
