@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
 import os
 from types import SimpleNamespace
 
@@ -50,6 +51,7 @@ STATIC_WS_BYTES = 64 << 20
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lib = None
+_fast = None
 
 
 class KDAError(RuntimeError):
@@ -565,8 +567,30 @@ def _expect(name, t, shape, dtype):
         raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
 
 
-# A small call's time is the host's, so the wrappers below ask each question once, in one
-# expression; only a call that fails it goes through the refusals that name the tensor.
+# A small call's time is the host's.  Each wrapper below first offers its call to the compiled
+# short way (csrc/kda_fast.cpp), which makes the same checks and answers None where one does not
+# hold; what it leaves (a call to refuse, another device's tensors, given gradients) goes on here.
+
+def _load_fast():
+    """The compiled short way (built with libkda.so); raise if absent."""
+    global _fast
+    if _fast is None:
+        load_library()
+        path = os.path.join(_HERE, "_kda_fast.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"_kda_fast.so is not built ({path}); run gated_delta_rule_85_b200/build.py")
+        spec = importlib.util.spec_from_file_location("_kda_fast", path)
+        _fast = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_fast)
+    return _fast
+
+
+def _done(r):
+    """The short way's answer, or the C ABI's error."""
+    if type(r) is int:
+        raise KDAError(r, last_error())
+    return r
+
 
 def _placed(index, tensors):
     """Every given tensor is a contiguous one on CUDA device `index`."""
@@ -652,6 +676,9 @@ def la_chunk_forward(q, k, v, log_decay, init_state=None, cu_seqlens=None, *, o=
     (uint8, la_workspace_size bytes) is allocated here unless given.
     Returns (o, final_state or None).
     """
+    r = (_fast or _load_fast()).la_forward(q, k, v, log_decay, init_state, cu_seqlens, o, final_state, workspace)
+    if r is not None:
+        return _done(r)
     B, T, H, dk, dv, N, dt = _la_shapes(q, k, v, log_decay, cu_seqlens)
     state = (N, H, dk, dv)
     if init_state is not None:
@@ -680,6 +707,9 @@ def la_chunk_forward_slots(q, k, v, log_decay, state_pool, slots, cu_seqlens=Non
     """la_chunk_forward from and into a state pool (kda_la_chunk_forward_slots): sequence n
     starts from state_pool[slots[n]] and its final state is written back there (slot -1:
     start from zeros, write nothing).  Returns o."""
+    r = (_fast or _load_fast()).la_forward_slots(q, k, v, log_decay, state_pool, slots, cu_seqlens, o, workspace)
+    if r is not None:
+        return _done(r)
     B, T, H, dk, dv, N, dt = _la_shapes(q, k, v, log_decay, cu_seqlens)
     _expect("state_pool", state_pool, (*state_pool.shape[:1], H, dk, dv), torch.float32)
     _expect("slots", slots, (N,), torch.int32)
@@ -707,6 +737,11 @@ def la_chunk_backward(q, k, v, log_decay, d_o, init_state=None, dfinal_state=Non
     d_o has o's shape and dtype, dfinal_state is float32 [N, H, dk, dv] or None (zero).  The
     workspace and the outputs (`out`, a dict with any of the keys) are allocated here unless given.
     """
+    if not out:
+        r = (_fast or _load_fast()).la_backward(q, k, v, log_decay, d_o, init_state, dfinal_state, cu_seqlens,
+                                                dinit_state, workspace)
+        if r is not None:
+            return _done(r)
     B, T, H, dk, dv, N, dt = _la_shapes(q, k, v, log_decay, cu_seqlens)
     dev = q.device
     state = (N, H, dk, dv)
@@ -760,6 +795,9 @@ def _la_step_shapes(q, k, v, log_decay, name, state, rows, o):
 def la_recurrent_step(q, k, v, log_decay, state, o=None):
     """One token of linear attention with a decay for each head (kda_la_recurrent_step);
     `state` [N, H, dk, dv] float32 is updated in place.  Returns o."""
+    r = (_fast or _load_fast()).la_step(q, k, v, log_decay, state, None, o)
+    if r is not None:
+        return _done(r)
     N, H, dk, dv, dt, o = _la_step_shapes(q, k, v, log_decay, "state", state, 0, o)
     index = q.get_device()
     if not _placed(index, (q, k, v, log_decay, state, o)):
@@ -772,6 +810,9 @@ def la_recurrent_step(q, k, v, log_decay, state, o=None):
 def la_recurrent_step_slots(q, k, v, log_decay, state_pool, slots, o=None):
     """la_recurrent_step on a state pool (kda_la_recurrent_step_slots): sequence n uses and
     updates state_pool[slots[n]] in place (slot -1: padding, o row zero).  Returns o."""
+    r = (_fast or _load_fast()).la_step(q, k, v, log_decay, state_pool, slots, o) if slots is not None else None
+    if r is not None:
+        return _done(r)
     N, H, dk, dv, dt, o = _la_step_shapes(q, k, v, log_decay, "state_pool", state_pool, None, o)
     _expect("slots", slots, (N,), torch.int32)
     index = q.get_device()
@@ -826,6 +867,9 @@ def group_norm(x, num_groups, weight=None, bias=None, gate=None, *, eps=1e-5, ac
     the heads of an attention output viewed as [B T, H dv] with num_groups = H), weight and
     bias float32 [C].  Returns (y, mean, rstd), the statistics float32 [N, num_groups].
     """
+    r = (_fast or _load_fast()).norm(x, num_groups, weight, bias, gate, eps, ACTIVATIONS.get(activation), y, workspace)
+    if r is not None:
+        return _done(r)
     N, L, C, dt, act = _norm_shapes(x, num_groups, weight, bias, gate, activation)
     if not eps > 0:
         raise ValueError(f"eps must be above 0, got {eps}")
@@ -849,6 +893,11 @@ def group_norm_backward(dy, x, mean, rstd, num_groups, weight=None, bias=None, g
     """Gradients of sum <dy, y> through group_norm (kda_group_norm_backward): a dict with dx,
     dweight and dbias (float32, when weight, bias are given) and dgate (with a gate).
     `mean` and `rstd` are what group_norm returned; `out` may hold any of the outputs."""
+    if not out:
+        r = (_fast or _load_fast()).norm_backward(dy, x, mean, rstd, num_groups, weight, bias, gate,
+                                                  ACTIVATIONS.get(activation), workspace)
+        if r is not None:
+            return _done(r)
     N, L, C, dt, act = _norm_shapes(x, num_groups, weight, bias, gate, activation)
     dev = x.device
     _expect("dy", dy, x.shape, x.dtype)

@@ -1,4 +1,5 @@
-"""Builds libkda.so (the C ABI of include/kda.h) in-tree for sm_100a with nvcc."""
+"""Builds libkda.so (the C ABI of include/kda.h) in-tree for sm_100a with nvcc, and _kda_fast.so, the
+Python binding's short way to some of its calls, with the host compiler."""
 from __future__ import annotations
 
 import os
@@ -8,6 +9,7 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libkda.so")
+FAST = os.path.join(HERE, "_kda_fast.so")
 OBJ = os.path.join(HERE, "build")
 # Each unit compiles by itself, all at once; its object is kept while nothing that it includes is newer.
 UNITS = {
@@ -50,31 +52,51 @@ def _sources(unit: str):
     return [os.path.join(HERE, "csrc", f) for f in [unit, *UNITS[unit]]] + [os.path.join(ROOT, "include", "kda.h")]
 
 
+def _fast_command(out: str):
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension as ext
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    includes = [*ext.include_paths(), sysconfig.get_paths()["include"],
+                os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    return [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-isystem{i}" for i in includes],
+            "-o", out, os.path.join(HERE, "csrc", "kda_fast.cpp"), "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+            "-L", HERE, "-l:libkda.so", "-Wl,-rpath,$ORIGIN"]
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    if not force and not _newer(LIB, [f for u in UNITS for f in _sources(u)]):
+    fast_sources = [os.path.join(HERE, "csrc", "kda_fast.cpp"), os.path.join(ROOT, "include", "kda.h")]
+    stale = force or _newer(LIB, [f for u in UNITS for f in _sources(u)])
+    if not stale and not _newer(FAST, fast_sources):
         return LIB
-    os.makedirs(OBJ, exist_ok=True)
-    cc = nvcc()
     tag = f".tmp{os.getpid()}"
-    running = []
-    for unit in UNITS:
-        if not force and not _newer(_object(unit), _sources(unit)):
-            continue
-        cmd = [cc, *NVCC_FLAGS, *extra, "-I", os.path.join(ROOT, "include"), "-c", "-o", _object(unit) + tag,
-               os.path.join(HERE, "csrc", unit)]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        running.append((unit, cmd, subprocess.Popen(cmd)))
-    codes = [(unit, cmd, p.wait()) for unit, cmd, p in running]
-    for unit, cmd, rc in codes:
-        if rc:
-            raise subprocess.CalledProcessError(rc, cmd)
-        os.replace(_object(unit) + tag, _object(unit))
-    cmd = [cc, *NVCC_FLAGS[:2], "-shared", "-o", LIB + tag, *[_object(u) for u in UNITS]]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
-    os.replace(LIB + tag, LIB)
+
+    def run(cmds):
+        """All at once: (command, file that it makes)."""
+        running = []
+        for cmd, _ in cmds:
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            running.append(subprocess.Popen(cmd))
+        codes = [p.wait() for p in running]
+        for (cmd, target), rc in zip(cmds, codes):
+            if rc:
+                raise subprocess.CalledProcessError(rc, cmd)
+            os.replace(target + tag, target)
+
+    if stale:
+        os.makedirs(OBJ, exist_ok=True)
+        cc = nvcc()
+        run([([cc, *NVCC_FLAGS, *extra, "-I", os.path.join(ROOT, "include"), "-c", "-o", _object(unit) + tag,
+               os.path.join(HERE, "csrc", unit)], _object(unit))
+             for unit in UNITS if force or _newer(_object(unit), _sources(unit))])
+        run([([cc, *NVCC_FLAGS[:2], "-shared", "-Xlinker", "-soname=libkda.so", "-o", LIB + tag,
+               *[_object(u) for u in UNITS]], LIB)])
+    if force or _newer(FAST, fast_sources):
+        run([(_fast_command(FAST + tag), FAST)])
     return LIB
 
 
