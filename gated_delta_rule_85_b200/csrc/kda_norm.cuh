@@ -7,13 +7,18 @@
 //   t = dz w,  dx = rstd (t - m1 - xhat m2),  m1, m2 = means of t and t xhat over the group
 // All arithmetic is in fp32; y, dx and dgate are rounded once, at the store.
 //
-// Two forms.  Rows (L = 1, D in whole 16-byte vectors): a group is D contiguous elements
+// Three forms.  Rows (L = 1, D in whole 16-byte vectors): a group is D contiguous elements
 // held in the registers of part of a warp, one read and one write of every element.
+// Cluster (several positions of whole groups that fit the shared memory of up to eight CTAs):
+// a thread-block cluster holds one sample's block of groups, and its CTAs exchange their sums
+// through distributed shared memory; one kernel, one read of every element.
 // Positions (any L, C, D): sums of row tiles, then a second kernel that joins them per group
 // and reads x again (from L2 where it fits).
 #pragma once
 
 #include <algorithm>
+
+#include <cooperative_groups.h>
 
 #include "kda_common.cuh"
 #include "kda_launch.cuh"
@@ -790,6 +795,329 @@ __global__ void __launch_bounds__(kThreads) pos_back_apply_kernel(
     }
 }
 
+// ------------------------------------------------------------------ cluster form
+
+// CTA `rank` of a cluster of K takes rows [rank R, rank R + R) of one sample and one block of
+// whole groups: blockIdx.x = (n blocks + block) K + rank.
+struct CluGeo {
+    int L, C, G, D;
+    int blocks, cb;     // channel blocks of a sample, groups of a block
+    int K, R;
+};
+template <typename T>
+struct Clu {
+    static constexpr int VEC = vec_of<T>();
+    int rank, n, g0, ng, c0, w, r0, nr;   // first group, groups, first channel, channels, first row, rows
+    int tpr, rl, cl, rows;                // threads of a row; this thread's row lane and vector; row lanes
+    bool on;
+    __device__ __forceinline__ explicit Clu(const CluGeo &p) {
+        rank = blockIdx.x % p.K;
+        const int b = blockIdx.x / p.K, blk = b % p.blocks;
+        n = b / p.blocks;
+        g0 = blk * p.cb;
+        ng = min(p.cb, p.G - g0);
+        c0 = g0 * p.D;
+        w = ng * p.D;
+        r0 = rank * p.R;
+        nr = max(0, min(p.R, p.L - r0));
+        tpr = w / VEC;
+        rows = kThreads / tpr;
+        rl = threadIdx.x / tpr;
+        cl = threadIdx.x - rl * tpr;
+        on = rl < rows;
+    }
+    // element offset of this thread's vector in row r of the CTA's rows
+    __device__ __forceinline__ long long at(const CluGeo &p, int r) const {
+        return ((long long)n * p.L + r0 + r) * p.C + c0 + cl * VEC;
+    }
+    __device__ __forceinline__ int tile_at(int r) const { return r * w + cl * VEC; }
+};
+// f(r) over this thread's rows, four at a time
+template <int U, typename T, typename F>
+__device__ __forceinline__ void clu_rows(const Clu<T> &c, F &&f) {
+    if (c.on)
+        for (int r = c.rl; r < c.nr; r += U * c.rows) f(r);
+}
+// Sums over the row lanes of red[rows][w], in place, into red[parts][w] with `parts` = as many
+// as keep every thread busy.  Ends with a barrier.
+__device__ __forceinline__ int clu_fold_rows(float *red, int rows, int w) {
+    const int parts = max(1, min(rows, kThreads / w));
+    for (int i0 = 0; i0 < w * parts; i0 += kThreads) {   // more than once only where parts is 1
+        const int i = i0 + threadIdx.x, q = parts > 1 ? i / w : 0;
+        float v = 0.f;
+        if (i < w * parts)
+#pragma unroll 4
+            for (int r = q; r < rows; r += parts) v += red[r * w + i - q * w];
+        __syncthreads();   // what a thread writes another may have read: parts > 1 writes rows that others sum
+        if (i < w * parts) red[i] = v;
+    }
+    __syncthreads();
+    return parts;
+}
+// sum of one group's D channels of red[parts][w], by `lanes` lanes
+__device__ __forceinline__ float clu_group_sum(const float *red, int parts, int w, int first, int D, int sl, int lanes) {
+    float s = 0.f;
+    for (int q = 0; q < parts; ++q)
+#pragma unroll 4
+        for (int c = sl; c < D; c += lanes) s += red[q * w + first + c];
+    return lane_sum(s, lanes);
+}
+
+template <typename T, int ACT, bool GATE>
+__global__ void __launch_bounds__(kThreads) cluster_forward_kernel(CluGeo p, const T *__restrict__ x,
+                                                                   const float *__restrict__ weight,
+                                                                   const float *__restrict__ bias,
+                                                                   const T *__restrict__ gate, T *__restrict__ y,
+                                                                   float *__restrict__ mean, float *__restrict__ rstd,
+                                                                   float eps) {
+    namespace cg = cooperative_groups;
+    constexpr int VEC = vec_of<T>(), U = 8;
+    using V = Vec<T, VEC>;
+    extern __shared__ __align__(16) uint8_t clu_smem[];
+    __shared__ float2 local[kThreads], stat[kThreads];   // (mean, m2) of this CTA's rows; (mean, rstd)
+    const Clu<T> c(p);
+    float *red = reinterpret_cast<float *>(clu_smem);     // [rows][w]
+    T *tile = reinterpret_cast<T *>(clu_smem + (size_t)kThreads * VEC * 4);
+    cg::cluster_group cluster = cg::this_cluster();
+
+    float acc[VEC] = {};
+    clu_rows<U>(c, [&](int r) {
+        typename V::Raw raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (r + u * c.rows < c.nr) raw[u] = ld_raw<typename V::Raw>(x + c.at(p, r + u * c.rows));
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (r + u * c.rows < c.nr) {
+                float f[VEC];
+                V::open(raw[u], f);
+                *reinterpret_cast<typename V::Raw *>(tile + c.tile_at(r + u * c.rows)) = raw[u];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) acc[e] += f[e];
+            }
+    });
+    const int lanes = lanes_for(c.ng), sl = threadIdx.x & (lanes - 1);
+    const float inv_local = c.nr ? 1.f / ((float)c.nr * p.D) : 0.f;
+    // each group's sum of `acc` over the CTA
+    auto groups = [&](auto &&store) {
+        if (c.on)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) red[c.tile_at(c.rl) + e] = acc[e];
+        __syncthreads();
+        const int parts = clu_fold_rows(red, c.rows, c.w);
+        for (int q = (int)(threadIdx.x & ~31) / lanes; q < c.ng; q += kThreads / lanes) {
+            const int g = min(q + (int)(threadIdx.x & 31) / lanes, c.ng - 1);
+            const float v = clu_group_sum(red, parts, c.w, g * p.D, p.D, sl, lanes);
+            if (sl == 0) store(g, v);
+        }
+        __syncthreads();
+    };
+    groups([&](int g, float v) { local[g].x = v * inv_local; });
+    float m[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        m[e] = c.on ? local[(c.cl * VEC + e) / p.D].x : 0.f;
+        acc[e] = 0.f;
+    }
+    clu_rows<1>(c, [&](int r) {
+        float f[VEC];
+        load_vec<T, VEC>(tile + c.tile_at(r), f);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[e] = fmaf(f[e] - m[e], f[e] - m[e], acc[e]);
+    });
+    groups([&](int g, float v) { local[g].y = v; });
+    cluster.sync();
+    if ((int)threadIdx.x < c.ng) {
+        const int g = threadIdx.x;
+        const float inv = 1.f / ((float)p.L * p.D);
+        float2 v[8];
+        float cnt[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            v[k] = k < p.K ? *cluster.map_shared_rank(&local[g], k) : make_float2(0.f, 0.f);
+            cnt[k] = k < p.K ? (float)max(0, min(p.R, p.L - k * p.R)) * p.D : 0.f;
+        }
+        float mu = 0.f, q = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mu = fmaf(cnt[k], v[k].x, mu);
+        mu *= inv;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) q += fmaf(cnt[k] * (v[k].x - mu), v[k].x - mu, v[k].y);
+        const float rs = rsqrtf(q * inv + eps);
+        stat[g] = make_float2(mu, rs);
+        if (c.rank == 0) {
+            mean[(long long)c.n * p.G + c.g0 + g] = mu;
+            rstd[(long long)c.n * p.G + c.g0 + g] = rs;
+        }
+    }
+    auto token = cluster.barrier_arrive();   // nobody leaves while its sums are read
+    __syncthreads();
+    float sc[VEC], o[VEC];   // z = (x - m) sc + o
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        const int ch = c.cl * VEC + e;
+        const float2 v = c.on ? stat[ch / p.D] : make_float2(0.f, 0.f);
+        m[e] = v.x;
+        sc[e] = v.y * (weight && c.on ? weight[c.c0 + ch] : 1.f);
+        o[e] = bias && c.on ? bias[c.c0 + ch] : 0.f;
+    }
+    clu_rows<U>(c, [&](int r) {
+        typename V::Raw gr[U];
+        if (GATE)
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (r + u * c.rows < c.nr) gr[u] = ld_raw<typename V::Raw>(gate + c.at(p, r + u * c.rows));
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (r + u * c.rows < c.nr) {
+                float f[VEC], gv[VEC], out[VEC];
+                load_vec<T, VEC>(tile + c.tile_at(r + u * c.rows), f);
+                if (GATE) V::open(gr[u], gv);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float z = fmaf(f[e] - m[e], sc[e], o[e]);
+                    out[e] = GATE ? z * act<T, ACT>(gv[e]) : act<T, ACT>(z);
+                }
+                st_raw(y + c.at(p, r + u * c.rows), V::close(out));
+            }
+    });
+    cluster.barrier_wait(std::move(token));
+}
+
+// part: [N][2][C] sums of dz xhat and dz of each sample (dweight and dbias themselves when N = 1)
+template <typename T, int ACT, bool GATE>
+__global__ void __launch_bounds__(kThreads) cluster_backward_kernel(
+    CluGeo p, const T *__restrict__ dy, const T *__restrict__ x, const float *__restrict__ mean,
+    const float *__restrict__ rstd, const float *__restrict__ weight, const float *__restrict__ bias,
+    const T *__restrict__ gate, T *__restrict__ dx, T *__restrict__ dgate, float *__restrict__ part_w,
+    float *__restrict__ part_b, long long part_stride) {
+    namespace cg = cooperative_groups;
+    constexpr int VEC = vec_of<T>(), U = 4, NT = GATE ? 3 : 2;
+    using V = Vec<T, VEC>;
+    let_next_start();
+    extern __shared__ __align__(16) uint8_t clu_smem[];
+    __shared__ float2 stat[kThreads];   // (m1, m2) of the groups
+    const Clu<T> c(p);
+    // [rows][w] sums of dz xhat, then of dz; the first w of each become the CTA's channel sums, which the
+    // other CTAs read; then this thread block's totals
+    float *red_w = reinterpret_cast<float *>(clu_smem), *red_b = red_w + kThreads * VEC, *tot_w = red_b + kThreads * VEC,
+          *tot_b = tot_w + kThreads * VEC;
+    T *tile = reinterpret_cast<T *>(tot_b + kThreads * VEC);
+    const int plane = p.R * c.w;        // elements of one tensor's tile
+    cg::cluster_group cluster = cg::this_cluster();
+    float m[VEC], rs[VEC], wt[VEC], bs[VEC], dw[VEC] = {}, db[VEC] = {};
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        const int ch = c.c0 + (c.on ? c.cl * VEC + e : 0);
+        const long long i = (long long)c.n * p.G + ch / p.D;
+        m[e] = mean[i];
+        rs[e] = rstd[i];
+        wt[e] = weight ? weight[ch] : 1.f;
+        bs[e] = bias ? bias[ch] : 0.f;
+    }
+    clu_rows<U>(c, [&](int r) {
+        typename V::Raw raw[U][NT];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (r + u * c.rows < c.nr) {
+                const long long at = c.at(p, r + u * c.rows);
+                raw[u][0] = ld_raw<typename V::Raw>(x + at);
+                raw[u][1] = ld_raw<typename V::Raw>(dy + at);
+                if (GATE) raw[u][NT - 1] = ld_raw<typename V::Raw>(gate + at);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (r + u * c.rows < c.nr) {
+                float f[VEC], dv[VEC], gv[VEC], dg[VEC];
+#pragma unroll
+                for (int k = 0; k < NT; ++k)
+                    *reinterpret_cast<typename V::Raw *>(tile + k * plane + c.tile_at(r + u * c.rows)) = raw[u][k];
+                V::open(raw[u][0], f);
+                V::open(raw[u][1], dv);
+                if (GATE) V::open(raw[u][NT - 1], gv);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float h = (f[e] - m[e]) * rs[e];
+                    const float z = fmaf(h, wt[e], bs[e]);
+                    const float dz = back_act<T, ACT, GATE>(z, dv[e], GATE ? gv[e] : 0.f, dg[e]);
+                    dw[e] = fmaf(dz, h, dw[e]);
+                    db[e] += dz;
+                }
+                if (GATE) st_raw(dgate + c.at(p, r + u * c.rows), V::close(dg));
+            }
+    });
+    if (c.on)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            red_w[c.tile_at(c.rl) + e] = dw[e];
+            red_b[c.tile_at(c.rl) + e] = db[e];
+        }
+    __syncthreads();
+    const int parts = clu_fold_rows(red_w, c.rows, c.w);
+    clu_fold_rows(red_b, c.rows, c.w);
+    if (parts > 1) {
+        for (int i = threadIdx.x; i < c.w; i += kThreads) {   // (w < kThreads here)
+            float a = red_w[i], b = red_b[i];
+            for (int k = 1; k < parts; ++k) {
+                a += red_w[k * c.w + i];
+                b += red_b[k * c.w + i];
+            }
+            red_w[i] = a;
+            red_b[i] = b;
+        }
+    }
+    cluster.sync();
+    for (int i = threadIdx.x; i < c.w; i += kThreads) {
+        float va[8], vb[8], a = 0.f, b = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            va[k] = k < p.K ? *cluster.map_shared_rank(red_w + i, k) : 0.f;
+            vb[k] = k < p.K ? *cluster.map_shared_rank(red_b + i, k) : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            a += va[k];
+            b += vb[k];
+        }
+        if (c.rank == 0) {
+            if (part_w) part_w[c.n * part_stride + c.c0 + i] = a;
+            if (part_b) part_b[c.n * part_stride + c.c0 + i] = b;
+        }
+        const float wc = weight ? weight[c.c0 + i] : 1.f;
+        tot_w[i] = wc * a;
+        tot_b[i] = wc * b;
+    }
+    auto token = cluster.barrier_arrive();   // nobody leaves while its sums are read
+    __syncthreads();
+    const int lanes = lanes_for(c.ng), sl = threadIdx.x & (lanes - 1);
+    const float inv = 1.f / ((float)p.L * p.D);
+    for (int q = (int)(threadIdx.x & ~31) / lanes; q < c.ng; q += kThreads / lanes) {
+        const int g = min(q + (int)(threadIdx.x & 31) / lanes, c.ng - 1);
+        const float s1 = clu_group_sum(tot_b, 1, c.w, g * p.D, p.D, sl, lanes);
+        const float s2 = clu_group_sum(tot_w, 1, c.w, g * p.D, p.D, sl, lanes);
+        if (sl == 0) stat[g] = make_float2(s1 * inv, s2 * inv);
+    }
+    __syncthreads();
+    float2 mm[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) mm[e] = c.on ? stat[(c.cl * VEC + e) / p.D] : make_float2(0.f, 0.f);
+    clu_rows<1>(c, [&](int r) {
+        float f[VEC], dv[VEC], gv[VEC], out[VEC], dg;
+        load_vec<T, VEC>(tile + c.tile_at(r), f);
+        load_vec<T, VEC>(tile + plane + c.tile_at(r), dv);
+        if (GATE) load_vec<T, VEC>(tile + 2 * plane + c.tile_at(r), gv);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const float h = (f[e] - m[e]) * rs[e];
+            const float z = fmaf(h, wt[e], bs[e]);
+            const float dz = back_act<T, ACT, GATE>(z, dv[e], GATE ? gv[e] : 0.f, dg);
+            out[e] = rs[e] * (dz * wt[e] - mm[e].x - h * mm[e].y);
+        }
+        st_raw(dx + c.at(p, r), V::close(out));
+    });
+    cluster.barrier_wait(std::move(token));
+}
+
 // dweight (blockIdx.y 0) or dbias (1) from the rows form's partial sums [reps][2][C]: 32
 // channels a CTA, 32 warps over the partial sums.
 __global__ void __launch_bounds__(1024) rows_back_join_kernel(const float *__restrict__ part, int reps, long long C,
@@ -825,6 +1153,9 @@ constexpr int kSMs = 148;
 
 struct Plan {
     bool rows;          // rows form
+    bool cluster;       // cluster form
+    CluGeo c;
+    size_t smem;        // of a CTA of the cluster form
     RowsGeo r;
     int nv, row_blocks;
     PosGeo p;
@@ -834,9 +1165,47 @@ struct Plan {
 
 inline long long gcd_of(long long a, long long b) { return b ? gcd_of(b, a % b) : a; }
 
+// Cluster form: blocks of the fewest groups that are whole vectors and at least 64 bytes of a
+// row (a half-used sector costs more than it saves below that), and the fewest CTAs that leave
+// room for several an SM and fill the GPU.  Beyond eight CTAs' shared memory the positions form
+// takes over, and for gradients above kClusterGrad elements, where a CTA's chain of barriers
+// costs more than the second read.  Measured, us, cluster | positions, bf16:
+//   forward   3 x 4096 x 320, 32 groups 16 | 23;  8 x 512 x 512, 8 groups 12 | 16;  4 x 64 x 72 10 | 18
+//   gradients 3 x 4096 x 320 27 | 22;  8 x 512 x 512 22 | 16;  2 x 1021 x 640 fp32 14 | 16;  1 x 2 x 64 8 | 10
+constexpr size_t kClusterWant = 56 * 1024, kClusterSmem = 200 * 1024;
+constexpr long long kClusterGrad = 3 << 19;
+inline bool cluster_plan(long long N, int L, int C, int G, int esize, bool gated, bool backward, Plan &s) {
+    const int vw = 16 / esize, D = C / G, unit = vw / (int)gcd_of(D, vw);
+    if (C % vw || (backward && N * L * C > kClusterGrad)) return false;
+    int cb = unit;
+    while (cb < G && (long long)cb * D * esize < 64) cb += unit;
+    // wider while there are CTAs enough without it
+    const int tensors = backward ? (gated ? 3 : 2) : 1;
+    while (cb < G && N * ((G + 2 * cb - 1) / (2 * cb)) >= 2 * kSMs && (long long)2 * cb * D <= kThreads * vw &&
+           (size_t)L * 2 * cb * D * esize * tensors <= kClusterWant)
+        cb *= 2;
+    cb = std::min(cb, G);
+    const long long vecs = (long long)cb * D / vw;
+    if (vecs > kThreads || cb > kThreads) return false;
+    const int blocks = (G + cb - 1) / cb, rows = kThreads / (int)vecs;
+    const size_t fixed = (size_t)kThreads * vw * 4 * (backward ? 4 : 1);
+    for (int K = 1; K <= 8; K *= 2) {
+        const int R = (L + K - 1) / K;
+        const size_t smem = fixed + (size_t)R * cb * D * esize * tensors;
+        if (K < 8 && (smem > kClusterWant || (N * blocks * K < kSMs && R > rows))) continue;
+        if (smem > kClusterSmem) return false;
+        s.cluster = true;
+        s.c = CluGeo{L, C, G, D, blocks, cb, K, R};
+        s.smem = smem;
+        s.ws = backward && N > 1 ? (size_t)N * 2 * C * sizeof(float) : 0;
+        return N * blocks * K < (1ll << 31);
+    }
+    return false;
+}
+
 // Rows form up to four vectors a lane (D <= 1024 bf16, 512 fp32); beyond that, or with
 // several positions, the statistics span CTAs.
-inline Plan plan_of(long long N, int L, int C, int G, int esize, bool backward) {
+inline Plan plan_of(long long N, int L, int C, int G, int esize, bool gated, bool backward) {
     Plan s{};
     const int vw = 16 / esize, D = C / G;
     if (L == 1 && D % vw == 0 && D / vw <= 128) {
@@ -855,6 +1224,9 @@ inline Plan plan_of(long long N, int L, int C, int G, int esize, bool backward) 
         s.ws = backward ? (size_t)(s.r.step / G) * 2 * C * sizeof(float) : 0;
         return s;
     }
+    if (cluster_plan(N, L, C, G, esize, gated, backward, s)) return s;
+    s.cluster = false;
+    s.ws = 0;
     s.vec = C % vw == 0;
     PosGeo &p = s.p;
     p.N = (int)N; p.L = L; p.C = C; p.G = G; p.D = D;
@@ -879,6 +1251,7 @@ struct Args {
     float *dweight, *dbias;
     float eps;
     void *ws;
+    long long N;
 };
 
 // Heads of 64 and 128 channels have kernels of their own widths.
@@ -895,6 +1268,24 @@ struct Args {
         KDA_ROWS(4, 0);                                       \
     }
 
+template <typename... Params, typename... A>
+cudaError_t launch_cluster(void (*kern)(Params...), const Plan &s, long long N, cudaStream_t st, A &&...args) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = s.c.K;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(N * s.c.blocks * s.c.K));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = s.smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
+}
+
 template <typename T, int ACT, bool GATE>
 cudaError_t launch_forward(const Plan &s, const Args &a, cudaStream_t st) {
     constexpr int VW = vec_of<T>();
@@ -908,6 +1299,9 @@ cudaError_t launch_forward(const Plan &s, const Args &a, cudaStream_t st) {
 #undef KDA_ROWS
         return cudaGetLastError();
     }
+    if (s.cluster)
+        return launch_cluster(cluster_forward_kernel<T, ACT, GATE>, s, a.N, st, s.c, x, a.weight, a.bias, gate, y, a.mean,
+                              a.rstd, a.eps);
     const dim3 grid((unsigned)((long long)s.p.N * s.p.tiles), s.p.Z);
     float2 *part = (float2 *)a.ws;
     auto run = [&](auto moments, auto apply) {
@@ -938,6 +1332,16 @@ cudaError_t launch_backward(const Plan &s, const Args &a, cudaStream_t st) {
             return launch_after(rows_back_join_kernel, dim3((unsigned)((C + 31) / 32), 2), 1024, 0, st, part,
                                 s.r.step / s.r.G, C, a.dweight, a.dbias);
         return cudaGetLastError();
+    }
+    if (s.cluster) {
+        const bool one = a.N == 1, join = !one && (a.dweight || a.dbias);
+        float *part = (float *)a.ws;
+        const cudaError_t e = launch_cluster(cluster_backward_kernel<T, ACT, GATE>, s, a.N, st, s.c, dy, x, a.mean, a.rstd,
+                                             a.weight, a.bias, gate, dx, dgate, one ? a.dweight : join ? part : nullptr,
+                                             one ? a.dbias : join ? part + s.c.C : nullptr, 2ll * s.c.C);
+        if (e != cudaSuccess || !join) return e;
+        return launch_after(rows_back_join_kernel, dim3((unsigned)((s.c.C + 31) / 32), 2), 1024, 0, st, part, (int)a.N,
+                            (long long)s.c.C, a.dweight, a.dbias);
     }
     const long long tiles = (long long)s.p.N * s.p.tiles;
     const dim3 grid((unsigned)tiles, s.p.Z);

@@ -34,7 +34,10 @@ extern "C" {
 
 size_t kda_group_norm_workspace_size(long long N, int L, int C, int G, int dtype, int backward) {
     if (N < 1 || L < 1 || C < 1 || G < 1 || C % G || (dtype != KDA_BF16 && dtype != KDA_F32)) return 0;
-    return kda::norm::plan_of(N, L, C, G, dtype == KDA_BF16 ? 2 : 4, backward != 0).ws;
+    // (with and without a gate: the forms may differ)
+    const int es = dtype == KDA_BF16 ? 2 : 4;
+    return std::max(kda::norm::plan_of(N, L, C, G, es, false, backward != 0).ws,
+                    kda::norm::plan_of(N, L, C, G, es, true, backward != 0).ws);
 }
 
 int kda_group_norm_forward(const void *x, const float *weight, const float *bias, const void *gate, void *y,
@@ -45,11 +48,11 @@ int kda_group_norm_forward(const void *x, const float *weight, const float *bias
     if (!(eps > 0.f)) return fail(KDA_ERR_INVALID_ARG, "eps=%g must be above 0", (double)eps);
     if (N == 0) return KDA_OK;
     const int es = dtype == KDA_BF16 ? 2 : 4;
-    const kda::norm::Plan s = kda::norm::plan_of(N, L, C, G, es, false);
+    const kda::norm::Plan s = kda::norm::plan_of(N, L, C, G, es, gate != nullptr, false);
     if ((rc = check_workspace(workspace, ws_bytes, s.ws))) return rc;
     kda::norm::Args a{};
     a.x = x; a.gate = gate; a.weight = weight; a.bias = bias; a.y = y; a.mean = mean; a.rstd = rstd; a.eps = eps;
-    a.ws = workspace;
+    a.ws = workspace; a.N = N;
     const cudaError_t e = es == 2 ? kda::norm::launch<__nv_bfloat16>(s, a, act, false, (cudaStream_t)stream)
                                   : kda::norm::launch<float>(s, a, act, false, (cudaStream_t)stream);
     return e == cudaSuccess ? KDA_OK : cuda_fail(e, "group norm launch");
@@ -75,12 +78,12 @@ int kda_group_norm_backward(const void *dy, const void *x, const float *mean, co
     if ((dweight && !aligned(dweight, 4)) || (dbias && !aligned(dbias, 4)))
         return fail(KDA_ERR_MISALIGNED, "dweight or dbias is not 4-byte aligned");
     const int es = dtype == KDA_BF16 ? 2 : 4;
-    const kda::norm::Plan s = kda::norm::plan_of(N, L, C, G, es, true);
+    const kda::norm::Plan s = kda::norm::plan_of(N, L, C, G, es, gate != nullptr, true);
     if ((rc = check_workspace(workspace, ws_bytes, s.ws))) return rc;
     kda::norm::Args a{};
     a.dy = dy; a.x = x; a.gate = gate; a.weight = weight; a.bias = bias; a.y = dx; a.dgate = dgate;
     a.mean = const_cast<float *>(mean); a.rstd = const_cast<float *>(rstd); a.dweight = dweight; a.dbias = dbias;
-    a.ws = workspace;
+    a.ws = workspace; a.N = N;
     const cudaError_t e = es == 2 ? kda::norm::launch<__nv_bfloat16>(s, a, act, true, (cudaStream_t)stream)
                                   : kda::norm::launch<float>(s, a, act, true, (cudaStream_t)stream);
     return e == cudaSuccess ? KDA_OK : cuda_fail(e, "group norm backward launch");

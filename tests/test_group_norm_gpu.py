@@ -218,3 +218,14 @@ def test_behind_the_attention(dtype):
     for n, (x, ref) in got.items():
         rel = float((x.detach().double() - ref.detach()).norm() / ref.detach().norm())
         assert rel <= tol, (n, rel)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("shape,G", [
+    ((2, 1021, 640), 32), ((3, 4096, 320), 32), ((1, 9000, 24), 3), ((300, 3, 64), 4),   # one cluster of one to eight CTAs
+    ((40, 2, 32), 32), ((1, 17, 2048), 1), ((2, 5, 2048), 2), ((1, 7, 4096), 1),            # widest rows, single-element groups
+    ((1, 30000, 64), 1), ((2, 200, 1000), 8), ((1, 2500, 1030), 5),                         # beyond a cluster, odd widths
+])
+@pytest.mark.parametrize("gate", [False, True])
+def test_forms_over_positions(dtype, shape, G, gate):
+    _check(_inputs(shape, dtype, seed=sum(shape), gate=gate), G, "silu", dtype)

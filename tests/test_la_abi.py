@@ -105,7 +105,7 @@ def test_step_slots_rejects(lib):
 
 
 def norm(lib, **over):
-    a = dict(x=A[0], w=A[1], b=A[2], gate=A[3], y=A[4], m=A[5], r=A[6], N=8, L=16, C=64, G=4, eps=1e-5, act=1, dtype=0,
+    a = dict(x=A[0], w=A[1], b=A[2], gate=A[3], y=A[4], m=A[5], r=A[6], N=8, L=100000, C=64, G=4, eps=1e-5, act=1, dtype=0,
              ws=A[7], wsb=WS)
     a.update(over)
     return lib.kda_group_norm_forward(*(a[x] for x in ("x", "w", "b", "gate", "y", "m", "r", "N", "L", "C", "G", "eps",
@@ -125,7 +125,7 @@ def test_norm_rejects(lib, over, code):
 
 
 def norm_back(lib, **over):
-    a = dict(dy=A[0], x=A[1], m=A[2], r=A[3], w=A[4], b=A[5], gate=A[6], dx=A[7], dg=A[8], dw=A[9], db=A[10], N=8, L=16,
+    a = dict(dy=A[0], x=A[1], m=A[2], r=A[3], w=A[4], b=A[5], gate=A[6], dx=A[7], dg=A[8], dw=A[9], db=A[10], N=8, L=100000,
              C=64, G=4, act=1, dtype=0, ws=A[11], wsb=WS)
     a.update(over)
     return lib.kda_group_norm_backward(*(a[x] for x in ("dy", "x", "m", "r", "w", "b", "gate", "dx", "dg", "dw", "db",
