@@ -504,10 +504,6 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
     const Carry &y = role.y;
     const bool want_last = y.last != nullptr;
 
-    if (warp == 1) {
-        ptx::tmem_alloc(ptx::smem_u32(tslot), 512);
-        ptx::tmem_relinquish();
-    }
     if (tid == 0) {
         for (int s = 0; s < NST; ++s) {
             ptx::mbar_init(bar_full + 8 * s, 1);
@@ -525,6 +521,12 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
         ptx::mbar_init(bar_fin, 1);
         ptx::fence_mbar_init();
     }
+    // before any tensor memory is taken: what waits holds nothing that the kernels it waits for may need
+    wait_for_previous();
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_u32(tslot), 512);
+        ptx::tmem_relinquish();
+    }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -533,7 +535,6 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
     SpanWalk it(g, w, dir);
     bool ok = true;
     int n = 0;   // chunks so far
-    wait_for_previous();
 
     if (warp == 0) {
         // ---------------- producer, and the sender of outputs
@@ -799,7 +800,7 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
             }
             if (it.first) {
                 const float *src = nullptr;
-                const int row = state_row(slots, num_slots, it.cur.n);
+                const int row = state_row(slots, num_slots, it.cur.n, 192);   // (the group's first thread)
                 if (it.from_before) src = y.start + (long long)w * DAB * DC;
                 else if (y.s0_copy && !it.whole) src = y.s0_copy + ((long long)it.cur.n * g.H + h) * (DAB * DC);
                 else if (y.s0 && row >= 0) src = y.s0 + ((long long)row * g.H + h) * (DAB * DC);
@@ -918,7 +919,7 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
                     }
                 }
                 if (it.ends && it.whole && want_last && has) {
-                    const int row = state_row(slots, num_slots, it.cur.n);
+                    const int row = state_row(slots, num_slots, it.cur.n, 192);
                     if (row >= 0) {
                         float *dst = y.last + (((long long)row * g.H + h) * DAB + r) * DC + col;
 #pragma unroll

@@ -13,7 +13,8 @@ int check_norm(const void *x, const void *y, const float *mean, const float *rst
     if (act != KDA_ACT_NONE && act != KDA_ACT_SILU && act != KDA_ACT_SIGMOID)
         return fail(KDA_ERR_INVALID_ARG, "act=%d is not a KDA_ACT_* value", act);
     if (dtype != KDA_BF16 && dtype != KDA_F32) return fail(KDA_ERR_UNSUPPORTED, "dtype=%d", dtype);
-    if (C > (1 << 24) || L > (1 << 30)) return fail(KDA_ERR_UNSUPPORTED, "C=%d above 2^24 or L=%d above 2^30", C, L);
+    if (C > 65535 * 256 || L > (1 << 30))   // (65535 blocks of 256 channels)
+        return fail(KDA_ERR_UNSUPPORTED, "C=%d above 16776960 or L=%d above 2^30", C, L);
     if (N > (1LL << 31) / G / 2 || N > 1LL << 24)
         return fail(KDA_ERR_UNSUPPORTED, "N=%lld with G=%d: at most 2^24 samples and 2^30 groups", N, G);
     if (N == 0) return KDA_OK;

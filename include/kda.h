@@ -453,7 +453,12 @@ int kda_gdn_chunk_backward_ex(const void *q, const void *k, const void *v, const
  * KDA_BF16 runs on the tensor cores with fp32 accumulation: o is rounded once more
  * than bf16 inputs need (the decayed scores and the state that o reads are bf16
  * operands), while final_state keeps fp32 accuracy.  KDA_F32 runs in fp32.
- * Rows of o behind the last packed sequence are not written.
+ * Rows of o behind the last packed sequence are not written.  A NaN or an infinity in a
+ * sequence's tokens or state stays in that sequence, where it may also reach outputs of
+ * up to 127 earlier tokens (a masked product of it is not zero).
+ * The outputs and the final state do not depend on which of them is asked for, and are
+ * the same bits every time.  No workspace is needed while T is at most one chunk (128
+ * tokens in KDA_BF16, 64 in KDA_F32).
  */
 size_t kda_la_chunk_forward_workspace_size(int B, int T, int H, int dk, int dv, int num_seqs, int dtype,
                                            int with_slots);
@@ -523,7 +528,8 @@ int kda_group_norm_forward(const void *x, const float *weight, const float *bias
                            int dtype, void *workspace, size_t ws_bytes, void *stream);
 
 /* Gradients of sum <dy, y>: dx and dgate (required with a gate) in dtype, dweight and
- * dbias fp32 [C] (each may be NULL), overwritten.  The same sums in the same order every time. */
+ * dbias fp32 [C] (each may be NULL), overwritten.  The same sums in the same order every time.
+ * The workspace size covers calls with and without a gate. */
 int kda_group_norm_backward(const void *dy, const void *x, const float *mean, const float *rstd,
                             const float *weight, const float *bias, const void *gate, void *dx, void *dgate,
                             float *dweight, float *dbias, long long N, int L, int C, int G, int act, int dtype,

@@ -155,6 +155,82 @@ def test_slots(dtype, cu):
     assert kda.device_status() == 0
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [1, 60, 300])
+def test_bad_slot_is_flagged(dtype, T):
+    """Whether a sequence is cut between CTAs or not; its rows are those of a start from zeros."""
+    d = lm.inputs(2, T, 2, 64, 64, dtype, seed=T)
+    pool = torch.randn(3, 2, 64, 64, device="cuda")
+    before = pool.clone()
+    d["S0"][0], d["S0"][1] = pool[2], 0
+    for bad in (3, -2, 2 ** 31 - 1):
+        pool.copy_(before)
+        slots = torch.tensor([2, bad], dtype=torch.int32, device="cuda")
+        o = kda.la_chunk_forward_slots(d["q"], d["k"], d["v"], d["log_decay"], pool, slots)
+        assert kda.device_status() == kda.DEV_BAD_SLOT
+        (o_ref, _), (Mo, _) = lm.reference(d)
+        lm.check(o, o_ref, lm.bound(o_ref, Mo, dtype, _terms(T, 64)), "o")
+        assert torch.equal(pool[:2], before[:2])
+        one = kda.la_recurrent_step_slots(*(d[x][:, 0].contiguous() for x in "qkv"), d["log_decay"], pool, slots)
+        assert (one[1] == 0).all()
+        assert kda.device_status() == kda.DEV_BAD_SLOT
+    assert kda.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_malformed_offsets_stay_in_bounds(dtype):
+    """Offsets that fall, leave the tokens or are negative: every access is clamped, rows around
+    the tensors stay, and a well-formed call behind is right."""
+    T, N = 500, 4
+    d = lm.inputs(1, T, 3, 64, 128, dtype, seed=1, N=N)
+    big = {x: torch.full((T + 64, *d[y].shape[2:]), 7.0, dtype=dtype, device="cuda")
+           for x, y in (("o", "v"), ("dq", "q"), ("dk", "k"), ("dv", "v"))}
+    at = {x: t[32:32 + T].unsqueeze(0) for x, t in big.items()}
+    for cu in ([0, 400, 100, 500, 300], [-5, 200, 900, 3, 500], [500, 0, 500, 0, 500], [2 ** 31 - 1, -2 ** 31, 0, 7, 9]):
+        cu_t = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        a = (d["q"], d["k"], d["v"], d["log_decay"])
+        kda.la_chunk_forward(*a, d["S0"], cu_t, o=at["o"])
+        kda.la_chunk_backward(*a, d["d_o"], d["S0"], d["dS"], cu_t, out={x: at[x] for x in ("dq", "dk", "dv")})
+        torch.cuda.synchronize()
+        for x, t in big.items():
+            assert (t[:32] == 7.0).all() and (t[32 + T:] == 7.0).all(), x
+    assert kda.device_status() == 0
+    cu = [0, 100, 100, 300, 500]
+    o, S = kda.la_chunk_forward(*a, d["S0"], torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    _check_prefill(d, o, S, dtype, cu)
+
+
+def test_short_way_and_long_way_agree():
+    """Calls that the compiled short way leaves to Python (outputs of gradients given, a workspace
+    of another type) give the same bits; errors of the C ABI come through either."""
+    d = lm.inputs(1, 200, 2, 64, 64, BF16, seed=9)
+    a = (d["q"], d["k"], d["v"], d["log_decay"])
+    g1 = kda.la_chunk_backward(*a, d["d_o"], d["S0"], d["dS"])
+    out = {x: torch.empty_like(t) for x, t in g1.items()}
+    g2 = kda.la_chunk_backward(*a, d["d_o"], d["S0"], d["dS"], out=dict(out))
+    for x in g1:
+        assert torch.equal(g1[x], g2[x]) and g2[x].data_ptr() == out[x].data_ptr()
+    o1, S1 = kda.la_chunk_forward(*a, d["S0"])
+    o2, S2 = torch.empty_like(o1), torch.empty_like(S1)
+    ws = torch.empty(kda.la_workspace_size(1, 200, 2, 64, 64, 1) // 4 + 64, dtype=torch.float32, device="cuda")
+    r = kda.la_chunk_forward(*a, d["S0"], o=o2, final_state=S2, workspace=ws)
+    assert r[0] is o2 and r[1] is S2 and torch.equal(o1, o2) and torch.equal(S1, S2)
+    with pytest.raises(kda.KDAError, match="workspace"):
+        kda.la_chunk_forward(*a, d["S0"], workspace=ws[:16])
+    odd = torch.empty(d["q"].numel() + 1, dtype=BF16, device="cuda")[1:].view_as(d["q"])
+    with pytest.raises(kda.KDAError, match="aligned"):
+        kda.la_chunk_forward(odd, *a[1:], d["S0"])
+    with pytest.raises(ValueError, match="contiguous"):
+        kda.la_chunk_forward(d["q"].expand(1, 200, 2, 64).transpose(1, 2).contiguous().transpose(1, 2), *a[1:], d["S0"])
+    with pytest.raises(ValueError, match="float32"):
+        kda.la_chunk_forward(*a, d["S0"].double())
+    with pytest.raises(ValueError, match="slots"):
+        kda.la_recurrent_step_slots(*(d[x][:, 0].contiguous() for x in "qkv"), d["log_decay"], d["S0"],
+                                    torch.zeros(1, dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError, match="is on cpu"):
+        kda.la_chunk_forward(d["q"], d["k"].cpu(), *a[2:], d["S0"])
+
+
 def _check_grads(d, g, dtype, cu=None, with_S0=True, with_dS=True, dinit=True):
     want, M = lm.reference_backward(d, cu, with_S0, with_dS)
     n = _terms(d["q"].shape[1], max(d["q"].shape[3], d["v"].shape[3]))
