@@ -60,16 +60,9 @@ struct Cursor {
         return min(max(g.cu[n], 0), g.T) / C + n;
     }
 
-    // Not inlined, as it runs once a sequence and every copy of it takes room from the kernels'
-    // loops; it fills another cursor, so that this one stays in registers.
     __device__ __forceinline__ void seek(const Geo &g, long long u) {
-        Cursor c;
-        find(g, u, c);
-        *this = c;
-    }
-    __device__ __noinline__ static void find(const Geo &g, long long u, Cursor &c) { c.find_item(g, u); }
-    __device__ __forceinline__ void find_item(const Geo &g, long long u) {
-        h = (int)(u / g.nslots);
+        // (a 64-bit division takes a thousand cycles where its instructions are not yet cached)
+        h = (u | g.nslots) >> 32 ? (int)(u / g.nslots) : (int)((unsigned)u / (unsigned)g.nslots);
         slot = (int)(u - (long long)h * g.nslots);
         if (!g.cu) {
             nck = (g.T + C - 1) / C;
