@@ -803,6 +803,7 @@ struct CluGeo {
     int L, C, G, D;
     int blocks, cb;     // channel blocks of a sample, groups of a block
     int K, R;
+    float inv_D;        // for the group of a channel of the block: (i + 0.5) / D, exact below 2^20
 };
 template <typename T>
 struct Clu {
@@ -810,7 +811,11 @@ struct Clu {
     int rank, n, g0, ng, c0, w, r0, nr;   // first group, groups, first channel, channels, first row, rows
     int tpr, rl, cl, rows;                // threads of a row; this thread's row lane and vector; row lanes
     bool on;
+    float inv_D;
+    // the group of a channel of the block
+    __device__ __forceinline__ int group(int ch) const { return (int)(((float)ch + 0.5f) * inv_D); }
     __device__ __forceinline__ explicit Clu(const CluGeo &p) {
+        inv_D = p.inv_D;
         rank = blockIdx.x % p.K;
         const int b = blockIdx.x / p.K, blk = b % p.blocks;
         n = b / p.blocks;
@@ -871,7 +876,7 @@ __global__ void __launch_bounds__(kThreads) cluster_forward_kernel(CluGeo p, con
                                                                    float *__restrict__ mean, float *__restrict__ rstd,
                                                                    float eps) {
     namespace cg = cooperative_groups;
-    constexpr int VEC = vec_of<T>(), U = 8;
+    constexpr int VEC = vec_of<T>(), U = 4;
     using V = Vec<T, VEC>;
     extern __shared__ __align__(16) uint8_t clu_smem[];
     __shared__ float2 local[kThreads], stat[kThreads];   // (mean, m2) of this CTA's rows; (mean, rstd)
@@ -916,7 +921,7 @@ __global__ void __launch_bounds__(kThreads) cluster_forward_kernel(CluGeo p, con
     float m[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-        m[e] = c.on ? local[(c.cl * VEC + e) / p.D].x : 0.f;
+        m[e] = c.on ? local[c.group(c.cl * VEC + e)].x : 0.f;
         acc[e] = 0.f;
     }
     clu_rows<1>(c, [&](int r) {
@@ -926,7 +931,7 @@ __global__ void __launch_bounds__(kThreads) cluster_forward_kernel(CluGeo p, con
         for (int e = 0; e < VEC; ++e) acc[e] = fmaf(f[e] - m[e], f[e] - m[e], acc[e]);
     });
     groups([&](int g, float v) { local[g].y = v; });
-    cluster.sync();
+    if (p.K > 1) cluster.sync();
     if ((int)threadIdx.x < c.ng) {
         const int g = threadIdx.x;
         const float inv = 1.f / ((float)p.L * p.D);
@@ -950,13 +955,13 @@ __global__ void __launch_bounds__(kThreads) cluster_forward_kernel(CluGeo p, con
             rstd[(long long)c.n * p.G + c.g0 + g] = rs;
         }
     }
-    auto token = cluster.barrier_arrive();   // nobody leaves while its sums are read
+    if (p.K > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");   // nobody leaves while its sums are read
     __syncthreads();
     float sc[VEC], o[VEC];   // z = (x - m) sc + o
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
         const int ch = c.cl * VEC + e;
-        const float2 v = c.on ? stat[ch / p.D] : make_float2(0.f, 0.f);
+        const float2 v = c.on ? stat[c.group(ch)] : make_float2(0.f, 0.f);
         m[e] = v.x;
         sc[e] = v.y * (weight && c.on ? weight[c.c0 + ch] : 1.f);
         o[e] = bias && c.on ? bias[c.c0 + ch] : 0.f;
@@ -981,7 +986,7 @@ __global__ void __launch_bounds__(kThreads) cluster_forward_kernel(CluGeo p, con
                 st_raw(y + c.at(p, r + u * c.rows), V::close(out));
             }
     });
-    cluster.barrier_wait(std::move(token));
+    if (p.K > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
 // part: [N][2][C] sums of dz xhat and dz of each sample (dweight and dbias themselves when N = 1)
@@ -1008,8 +1013,8 @@ __global__ void __launch_bounds__(kThreads) cluster_backward_kernel(
     float m[VEC], rs[VEC], wt[VEC], bs[VEC], dw[VEC] = {}, db[VEC] = {};
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-        const int ch = c.c0 + (c.on ? c.cl * VEC + e : 0);
-        const long long i = (long long)c.n * p.G + ch / p.D;
+        const int in = c.on ? c.cl * VEC + e : 0, ch = c.c0 + in;
+        const long long i = (long long)c.n * p.G + c.g0 + c.group(in);
         m[e] = mean[i];
         rs[e] = rstd[i];
         wt[e] = weight ? weight[ch] : 1.f;
@@ -1066,7 +1071,8 @@ __global__ void __launch_bounds__(kThreads) cluster_backward_kernel(
             red_b[i] = b;
         }
     }
-    cluster.sync();
+    if (p.K > 1) cluster.sync();
+    else __syncthreads();
     for (int i = threadIdx.x; i < c.w; i += kThreads) {
         float va[8], vb[8], a = 0.f, b = 0.f;
 #pragma unroll
@@ -1087,7 +1093,7 @@ __global__ void __launch_bounds__(kThreads) cluster_backward_kernel(
         tot_w[i] = wc * a;
         tot_b[i] = wc * b;
     }
-    auto token = cluster.barrier_arrive();   // nobody leaves while its sums are read
+    if (p.K > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");   // nobody leaves while its sums are read
     __syncthreads();
     const int lanes = lanes_for(c.ng), sl = threadIdx.x & (lanes - 1);
     const float inv = 1.f / ((float)p.L * p.D);
@@ -1100,7 +1106,7 @@ __global__ void __launch_bounds__(kThreads) cluster_backward_kernel(
     __syncthreads();
     float2 mm[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) mm[e] = c.on ? stat[(c.cl * VEC + e) / p.D] : make_float2(0.f, 0.f);
+    for (int e = 0; e < VEC; ++e) mm[e] = c.on ? stat[c.group(c.cl * VEC + e)] : make_float2(0.f, 0.f);
     clu_rows<1>(c, [&](int r) {
         float f[VEC], dv[VEC], gv[VEC], out[VEC], dg;
         load_vec<T, VEC>(tile + c.tile_at(r), f);
@@ -1115,7 +1121,7 @@ __global__ void __launch_bounds__(kThreads) cluster_backward_kernel(
         }
         st_raw(dx + c.at(p, r), V::close(out));
     });
-    cluster.barrier_wait(std::move(token));
+    if (p.K > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
 // dweight (blockIdx.y 0) or dbias (1) from the rows form's partial sums [reps][2][C]: 32
@@ -1195,7 +1201,7 @@ inline bool cluster_plan(long long N, int L, int C, int G, int esize, bool gated
         if (K < 8 && (smem > kClusterWant || (N * blocks * K < kSMs && R > rows))) continue;
         if (smem > kClusterSmem) return false;
         s.cluster = true;
-        s.c = CluGeo{L, C, G, D, blocks, cb, K, R};
+        s.c = CluGeo{L, C, G, D, blocks, cb, K, R, 1.f / D};
         s.smem = smem;
         s.ws = backward && N > 1 ? (size_t)N * 2 * C * sizeof(float) : 0;
         return N * blocks * K < (1ll << 31);
