@@ -40,11 +40,12 @@ struct Geo {
     const int32_t *cu;   // packed offsets, or null
     int T, N, H;         // tokens of a row (packed: of the call), sequences, heads
     int nslots;          // chunk slots of one head
-    int W;               // spans: `rem` of them have per + 1 items, the others per
+    int W;               // spans: `rem` of them have (per + 1) unit items, the others per unit
     int rem;
     long long per;
+    int unit;            // 1, or the chunks of a sequence: then no sequence is cut
     __host__ __device__ long long items() const { return (long long)H * nslots; }
-    __host__ __device__ long long lo(int w) const { return w * per + (w < rem ? w : rem); }
+    __host__ __device__ long long lo(int w) const { return unit * (w * per + (w < rem ? w : rem)); }
     __host__ __device__ long long hi(int w) const { return lo(w + 1); }
 };
 

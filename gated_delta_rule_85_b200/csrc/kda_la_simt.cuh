@@ -273,13 +273,38 @@ struct Call {
     cudaStream_t st;
 };
 
+// Cut spans give every SM the same share, but cost a first pass over k and v, a join and two
+// more launches.  A dense batch is cut only where whole sequences take longer, by a model in
+// chunks of one walk: `walks` walks and `sums` first passes, side by side in one launch or one
+// after the other.  Measured on the way to its constants, us, cut | whole:
+//   bf16 forward   2 x 300 x 32 heads of 128 39 | 25;  8 x 2048 x 32 222 | 165;  4 x 1000 x 8 37 | 47
+//   bf16 gradients 4 x 1000 x 8 heads of 128 75 | 48;  8 x 2048 x 32 532 | 402;  1 x 1500 x 4 29 | 63
+//   fp32 forward   8 x 500 x 16 heads of 64 164 | 91;  1 x 200 x 8 44 | 94
 template <int C>
-Geo geo_of(const Call &c) {
-    Geo g{c.cu, c.T, c.N, c.H, 0, 0, 0, 0};
-    g.nslots = (int)(c.cu ? (long long)c.T / C + c.N : (long long)c.N * ((c.T + C - 1) / C));
-    g.W = (int)std::min<long long>(g.items(), kSMs);
-    g.per = g.items() / g.W;
-    g.rem = (int)(g.items() % g.W);
+Geo geo_of(const Call &c, int walks, int sums, bool side_by_side) {
+    Geo g{c.cu, c.T, c.N, c.H, 0, 0, 0, 0, 1};
+    const int nck = (c.T + C - 1) / C;
+    g.nslots = (int)(c.cu ? (long long)c.T / C + c.N : (long long)c.N * nck);
+    if (!c.cu) {
+        auto rounds = [](long long ctas) { return (float)((ctas + kSMs - 1) / kSMs); };
+        const float sum = C == kSimtC ? 0.45f : 0.63f, fixed = C == kSimtC ? 0.5f : 1.9f;
+        const long long seqs = (long long)c.H * c.N, ctas = std::min<long long>(g.items(), kSMs);
+        const float part = rounds(g.items());   // the longest cut span
+        float cut = fixed, whole;
+        if (side_by_side) {
+            cut += (sum * rounds(sums * ctas) + rounds(walks * ctas)) * part;
+            whole = seqs <= kSMs ? rounds(walks * seqs)
+                                 : std::min(walks * rounds(seqs), (float)(walks * seqs) / kSMs + 1.f);
+        } else {
+            cut += (sum * sums + walks) * part;
+            whole = walks * rounds(seqs);
+        }
+        if (whole * nck <= cut) g.unit = nck;
+    }
+    const long long units = g.items() / g.unit;
+    g.W = (int)std::min<long long>(units, kSMs);
+    g.per = units / g.W;
+    g.rem = (int)(units % g.W);
     return g;
 }
 
@@ -287,7 +312,7 @@ Geo geo_of(const Call &c) {
 // more than one chunk may be cut.
 template <int C>
 bool cuts(const Geo &g) {
-    if (g.T <= C) return false;
+    if (g.T <= C || g.unit > 1) return false;
     if (g.cu) return true;
     const int per = (g.T + C - 1) / C;
     for (int w = 1; w < g.W; ++w)
@@ -344,7 +369,7 @@ cudaError_t launch_simt(const Geo &g, const Walk &wk, const Call &c, bool after 
 template <int DK, int DV, typename Tin>
 cudaError_t simt_forward(const Call &c, const void *q, const void *k, const void *v, const float *s0, void *o,
                          float *last, float *ws) {
-    const Geo g = geo_of<kSimtC>(c);
+    const Geo g = geo_of<kSimtC>(c, 1, 1, false);
     Walk wk{q, k, v, o, carry_at(ws, g.W, DK * DV), false};
     wk.y.s0 = s0;
     wk.y.last = last;
@@ -365,7 +390,7 @@ cudaError_t simt_forward(const Call &c, const void *q, const void *k, const void
 template <int DK, int DV, typename Tin>
 cudaError_t simt_backward(const Call &c, const void *q, const void *k, const void *v, const void *d_o, const float *s0,
                           const float *dlast, void *dq, void *dk, void *dv, float *dinit, float *ws) {
-    const Geo g = geo_of<kSimtC>(c);
+    const Geo g = geo_of<kSimtC>(c, 3, 2, false);
     constexpr int E = DK * DV;
     Carry fwd = carry_at(ws, g.W, E), bwd = carry_at(ws + (size_t)3 * g.W * E, g.W, E);
     fwd.s0 = s0;

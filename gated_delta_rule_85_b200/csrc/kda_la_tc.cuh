@@ -1036,7 +1036,7 @@ cudaError_t launch_walk(const Geo &g, const WalkArgs &a, int roles, const Call &
 template <int DK, int DV>
 cudaError_t tc_forward(const Call &c, const void *q, const void *k, const void *v, const float *s0, void *o,
                        float *last, float *ws) {
-    const Geo g = geo_of<kC>(c);
+    const Geo g = geo_of<kC>(c, 1, 1, true);
     CUtensorMap tq, tk, tv, to;
     if (!tile_map(&tq, q, c, DK) || !tile_map(&tk, k, c, DK) || !tile_map(&tv, v, c, DV) ||
         !tile_map(&to, o, c, DV, kOutBox))
@@ -1064,7 +1064,7 @@ cudaError_t tc_forward(const Call &c, const void *q, const void *k, const void *
 template <int DK, int DV>
 cudaError_t tc_backward(const Call &c, const void *q, const void *k, const void *v, const void *d_o, const float *s0,
                         const float *dlast, void *dq, void *dk, void *dv, float *dinit, float *ws) {
-    const Geo g = geo_of<kC>(c);
+    const Geo g = geo_of<kC>(c, 3, 2, true);
     constexpr int E = DK * DV;
     CUtensorMap tq, tk, tv, td, odq, odk, odv;
     if (!tile_map(&tq, q, c, DK) || !tile_map(&tk, k, c, DK) || !tile_map(&tv, v, c, DV) || !tile_map(&td, d_o, c, DV) ||

@@ -62,6 +62,25 @@ def test_decay_range(dtype, slopes):
     _check_grads(d, g, dtype)
 
 
+@pytest.mark.parametrize("dtype,T", [(BF16, 300), (F32, 150)])
+@pytest.mark.parametrize("slotted", [False, True])
+def test_dense_batches_of_whole_sequences(dtype, T, slotted):
+    """More sequences than SMs, each of several chunks: spans of one and of two whole ones."""
+    B, H = 10, 20
+    d = lm.inputs(B, T, H, 64, 64, dtype, seed=T)
+    a = (d["q"], d["k"], d["v"], d["log_decay"])
+    if slotted:
+        pool = torch.cat([d["S0"].flip(0), torch.zeros_like(d["S0"][:1])])
+        slots = torch.arange(B - 1, -1, -1, dtype=torch.int32, device="cuda")
+        o = kda.la_chunk_forward_slots(*a, pool, slots)
+        S = pool[:B].flip(0)
+    else:
+        o, S = kda.la_chunk_forward(*a, d["S0"])
+        g = kda.la_chunk_backward(*a, d["d_o"], d["S0"], d["dS"])
+        _check_grads(d, g, dtype)
+    _check_prefill(d, o, S, dtype)
+
+
 CUS = [[0, 70, 70, 199, 200, 264], [0, 0, 0, 5], [0, 1], [0, 128, 256, 384], [0, 300, 301, 301, 301, 650, 651],
        [0] + list(range(1, 41)) + [400]]
 
