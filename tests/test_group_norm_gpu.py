@@ -229,3 +229,37 @@ def test_behind_the_attention(dtype):
 @pytest.mark.parametrize("gate", [False, True])
 def test_forms_over_positions(dtype, shape, G, gate):
     _check(_inputs(shape, dtype, seed=sum(shape), gate=gate), G, "silu", dtype)
+
+
+@pytest.mark.parametrize("shape,G", [((2 ** 17 + 5, 128 * 128), 128), ((2 ** 19 + 3, 16, 256), 32), ((1, 2 ** 23 + 64, 256), 32),
+                                     ((2, 2 ** 22 + 64, 260), 5)],
+                         ids=["rows", "clusters", "positions", "odd_positions"])
+def test_elements_beyond_32_bits(shape, G):
+    """More than 2^31 elements.  x is +-1 in turn, so every mean is 0 and every variance 1, and an element
+    of the result is one of two values.  A thread's sums of ones are exact; the joins of at most 512 parts
+    round once each, which holds a mean and a variance to 2^-14."""
+    C = shape[-1]
+    sign = torch.ones(C, dtype=BF16, device="cuda")
+    sign[1::2] = -1
+    x = sign.expand(shape).contiguous()
+    y = torch.full_like(x, 7.0)
+    w, b = torch.full((C,), 1.5, device="cuda"), torch.full((C,), 0.25, device="cuda")
+    _, mean, rstd = kda.group_norm(x, G, w, b, activation="none", eps=EPS, y=y)
+    z = (1 + EPS) ** -0.5 * 1.5 * sign.double() + 0.25
+    assert (mean.abs() <= 2.0 ** -14).all() and ((rstd.double() - (1 + EPS) ** -0.5).abs() <= 2.0 ** -14).all()
+    flat = y.view(-1, C)
+    for part in (flat[:64], flat[-64:], flat[flat.shape[0] // 2 - 32:][:64]):
+        assert ((part.double() - z).abs() <= 2.0 ** -8 * z.abs() + 1.5 * 2.0 ** -13).all()
+    assert (y < 2).all()
+    # dy = x: the projection takes all of dx but w rstd eps / (1 + eps); its three terms are each at most
+    # 1.5 and carry the roundings of a group's sums
+    g = kda.group_norm_backward(x, x, mean, rstd, G, w, b, activation="none", out={"dx": y.fill_(7.0)})
+    M = x.numel() // C
+    n = M // shape[0] * (C // G)
+    lim = 3 * 1.5 * ((n / 32 + 64) * 2.0 ** -24 + 2.0 ** -13) + 2 * 1.5 * EPS
+    assert (y.abs() <= lim).all()
+    want = M * (1 + EPS) ** -0.5
+    assert ((g["dweight"].double() - want).abs() <= want * ((M / 32 + 64) * 2.0 ** -24 + 2.0 ** -13)).all()
+    assert ((g["dbias"].double() - M * sign.double()).abs() <= M * (M / 32 + 64) * 2.0 ** -24).all()
+    del x, y, g, flat
+    torch.cuda.empty_cache()

@@ -453,3 +453,56 @@ def test_long(T, H):
     g = kda.la_chunk_backward(d["q"], d["k"], d["v"], d["log_decay"], d["d_o"], d["S0"], d["dS"])
     torch.cuda.synchronize()
     _check_grads(d, g, BF16)
+
+
+def _some_heads(d, heads):
+    """The inputs of these heads alone."""
+    axis = {"S0": 1, "dS": 1, "log_decay": 0}
+    return {x: t.index_select(axis.get(x, 2), torch.tensor(heads, device="cuda")) for x, t in d.items()}
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_elements_beyond_32_bits(dtype):
+    """A last sequence whose elements all lie behind 2^31 others (zeros), and every state but the first."""
+    H, tail, heads = 128, 150, [0, 125, 127]
+    first = 2 ** 31 // (H * 128)
+    d = lm.inputs(1, tail, H, 128, 128, dtype, seed=21, N=2)
+    big = {x: torch.zeros(1, first + tail, H, 128, dtype=dtype, device="cuda") for x in ("q", "k", "v", "d_o")}
+    for x, t in big.items():
+        t[:, first:] = d[x]
+    d["S0"][0], d["dS"][0] = 0, 0
+    cu = torch.tensor([0, first, first + tail], dtype=torch.int32, device="cuda")
+    o, S = kda.la_chunk_forward(big["q"], big["k"], big["v"], d["log_decay"], d["S0"], cu)
+    g = kda.la_chunk_backward(big["q"], big["k"], big["v"], d["log_decay"], big["d_o"], d["S0"], d["dS"], cu)
+    torch.cuda.synchronize()
+    assert not S[0].any() and not g["dinit_state"][0].any() and not o[:, :first].any()
+    small = _some_heads({**d, "S0": d["S0"][1:], "dS": d["dS"][1:]}, heads)
+    _check_prefill(small, o[:, first:, heads], S[1:, heads], dtype)
+    got = {x: g[x][:, first:, heads] for x in ("dq", "dk", "dv")}
+    _check_grads(small, {**got, "dinit_state": g["dinit_state"][1:, heads]}, dtype)
+    del big, o, g
+    torch.cuda.empty_cache()
+
+
+def test_pool_beyond_32_bits():
+    """Slots behind 2^31 floats of the pool give what the first ones do."""
+    H = 128
+    rows = 2 ** 31 // (H * 128 * 128) + 2
+    d = lm.inputs(2, 150, H, 128, 128, BF16, seed=22)
+    a = (d["q"], d["k"], d["v"], d["log_decay"])
+    one = (*(d[x][:, 0].contiguous() for x in "qkv"), d["log_decay"])
+    pool = torch.zeros(rows, H, 128, 128, device="cuda")
+    got = []
+    for table in ([0, 1], [rows - 1, rows - 2]):
+        slots = torch.tensor(table, dtype=torch.int32, device="cuda")
+        pool[table] = d["S0"]
+        o = kda.la_chunk_forward_slots(*a, pool, slots)
+        after = pool[table]
+        step = kda.la_recurrent_step_slots(*one, pool, slots)
+        got.append((o, after, step, pool[table]))
+        pool[table] = 0
+        assert kda.device_status() == 0
+    assert all(torch.equal(x, y) for x, y in zip(*got))
+    assert not pool.any()
+    del pool
+    torch.cuda.empty_cache()
