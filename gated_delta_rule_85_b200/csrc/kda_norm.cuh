@@ -157,10 +157,13 @@ __device__ __forceinline__ float lane_sum(float x, int lanes) {
 // the same over LANES lanes, unrolled; LANES = 0: `lanes`
 template <int LANES>
 __device__ __forceinline__ float group_sum(float x, int lanes) {
-    if (LANES == 0) return lane_sum(x, lanes);
+    if constexpr (LANES == 0) {
+        return lane_sum(x, lanes);
+    } else {
 #pragma unroll
-    for (int o = LANES / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
+        for (int o = LANES / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        return x;
+    }
 }
 
 // ------------------------------------------------------------------ rows form
