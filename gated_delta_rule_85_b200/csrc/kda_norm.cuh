@@ -1279,7 +1279,8 @@ struct Args {
 
 template <typename... Params, typename... A>
 cudaError_t launch_cluster(void (*kern)(Params...), const Plan &s, long long N, cudaStream_t st, A &&...args) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem);
+    // one limit for every plan: another host thread may be between its own call of this and its launch
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kClusterSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
