@@ -109,6 +109,13 @@ struct Cursor {
     __device__ __forceinline__ int len() const { return (int)min((long long)C, t1 - tok()); }
 };
 
+// A head's rate.  Below -1e30 every power but the 0th is 0 all the same, and the products with
+// distances, also in fp32 and with 1 / log 2, stay finite (an infinite one times a distance of 0 is NaN).
+__device__ __forceinline__ float rate_of(const float *log_decay, int h) {
+    const float x = log_decay[h];
+    return x < -1e30f ? -1e30f : x;
+}
+
 // exp(log_decay e) with the exponent's product in 64 bits, as the sum of two floats:
 // a chunk's decay is applied once per chunk of a sequence, so an error in its last
 // place would grow with the number of chunks.
@@ -216,7 +223,7 @@ __global__ void __launch_bounds__(256) la_join_kernel(Geo g, const __grid_consta
             // behind the span where the sequence ends nothing is asked for
             dec[threadIdx.x] = threadIdx.x + base > 0 && !crossed(x - dir) && x - dir != w0
                                    ? make_float2(0.f, 0.f)
-                                   : decay2(log_decay[cur.h], tokens(x));
+                                   : decay2(rate_of(log_decay, cur.h), tokens(x));
         }
         __syncthreads();
     };

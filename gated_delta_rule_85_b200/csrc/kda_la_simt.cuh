@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(256) la_simt_kernel(Geo g, Walk wk, const floa
         __syncthreads();   // the chunk before is done with shared memory
         if (h != head) {
             head = h;
-            lg = log_decay[h];
+            lg = rate_of(log_decay, h);
             if (tid <= kSimtC) sm[L::PW + tid] = (float)exp((double)lg * tid);
         }
         if (first) {

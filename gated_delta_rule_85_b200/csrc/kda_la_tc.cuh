@@ -301,7 +301,7 @@ la_sum_kernel(const __grid_constant__ SumArgs args, Geo g, const float *__restri
         for (int q = 0; q < 2 && ok; ++q) {
             const Part &p = part[q];
             if (p.nt == 0) continue;
-            const double lg = (double)log_decay[p.h];
+            const double lg = (double)rate_of(log_decay, p.h);
             // forwards the weight counts from the tile's end, backwards from its start
             const Weight full_wt((float)exp64(lg * (dir > 0 ? kBox - 1 - jr : jr + 1)));
 #pragma unroll 1
@@ -363,7 +363,7 @@ la_sum_kernel(const __grid_constant__ SumArgs args, Geo g, const float *__restri
             if (p.nt == 0) continue;
 #pragma unroll
             for (int x = 0; x < CPT; ++x) S[x] = 0.f;
-            const double lg = (double)log_decay[p.h], full_dec = exp64(lg * kBox);
+            const double lg = (double)rate_of(log_decay, p.h), full_dec = exp64(lg * kBox);
             double behind = 1.0;         // decay of the tokens behind the tile
 #pragma unroll 1
             for (int x = 0; x < p.nt; ++x, ++n) {
@@ -727,7 +727,7 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
             if (len == 0) break;
             if (h != head) {
                 head = h;
-                l2 = log_decay[h] * 1.44269504f;
+                l2 = rate_of(log_decay, h) * 1.44269504f;
 #pragma unroll
                 for (int m = 0; m < 16; ++m) {
                     step[m] = kda::tc::exp2_fast(l2 * (dir > 0 ? 15 - m : m));
@@ -850,7 +850,7 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
             if (h != head || len != wlen) {
                 head = h;
                 wlen = len;
-                const float lg = log_decay[h];
+                const float lg = rate_of(log_decay, h);
                 wt = Weight(r < len ? (float)exp64((double)lg * (dir > 0 ? len - 1 - r : r + 1)) : 0.f);
                 dec = decay2(lg, len);
             }

@@ -444,7 +444,8 @@ int kda_gdn_chunk_backward_ex(const void *q, const void *k, const void *v, const
  * operator on the same buffers.
  *
  *   q, k, v, o    as in kda_chunk_forward
- *   log_decay     fp32 [H] on the device, <= 0 and finite (0: nothing is forgotten)
+ *   log_decay     fp32 [H] on the device, <= 0 (0: nothing is forgotten; minus infinity: everything,
+ *                 at each token)
  *   init_state, final_state, cu_seqlens, B, T, H, dk, dv, num_seqs, dtype
  *                 as in kda_chunk_forward
  *   workspace     kda_la_chunk_forward_workspace_size() bytes, 256-byte aligned
