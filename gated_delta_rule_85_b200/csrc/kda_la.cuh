@@ -116,6 +116,14 @@ __device__ __forceinline__ float rate_of(const float *log_decay, int h) {
     return x < -1e30f ? -1e30f : x;
 }
 
+// Flags entries of a slot table that are outside the pool: no span visits a packed sequence without
+// tokens.  A walk calls it with threads that have to wait for their first tiles anyway (not inlined: it costs
+// the loops behind it registers).
+__device__ __noinline__ void check_slots(int seqs, const int32_t *slots, int num_slots, int thread, int threads) {
+    for (int n = blockIdx.x * threads + thread; n < seqs; n += gridDim.x * threads)
+        if (slots[n] < -1 || slots[n] >= num_slots) flag_status(KDA_DEV_BAD_SLOT);
+}
+
 // exp(log_decay e) with the exponent's product in 64 bits, as the sum of two floats:
 // a chunk's decay is applied once per chunk of a sequence, so an error in its last
 // place would grow with the number of chunks.

@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(256) la_simt_kernel(Geo g, Walk wk, const floa
     const long long lo = g.lo(w), hi = g.hi(w);
     const long long E = DAB * DC;
     const Carry &y = wk.y;
+    if (WALK && DIR > 0 && g.cu && slots) check_slots(g.N, slots, num_slots, tid, 256);
 
     float S[RM][CG * 4];
     int head = -1;

@@ -709,6 +709,7 @@ la_walk_kernel(const __grid_constant__ WalkArgs args, Geo g, const float *__rest
     } else if (warp < 6) {
         // ---------------- scores -> P, accumulators -> out.  Thread <-> row i.
         const int quad = warp & 3, i = quad * 32 + lane;
+        if (g.cu && slots) check_slots(g.N, slots, num_slots, tid - 64, 128);
         auto wait_out = [&](uint32_t bar, uint32_t parity) { return wait_group<1, 128>(warp == 2, bar, parity); };
         const uint32_t tl = (uint32_t)(quad * 32) << 16;
         // Powers that a head keeps: in a 16-column block all on one side of the diagonal

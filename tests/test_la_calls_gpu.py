@@ -31,3 +31,24 @@ def test_lowest_rates(dtype, T):
     assert (g["dinit_state"] == 0).all()
     assert not lp.over(one.unsqueeze(1), o_ref[:, :1], lp.out_limit(dtype, 1, 128), 2)
     assert torch.equal(pool[0], d["k"][0, 0].float().unsqueeze(-1) * d["v"][0, 0].float().unsqueeze(-2))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [60, 300])
+def test_bad_slot_of_a_sequence_without_tokens(dtype, T):
+    """It is flagged like any other, whether a call's sequences are cut between CTAs or not."""
+    d = lm.inputs(1, T, 2, 64, 64, dtype, seed=T, N=3)
+    a = (d["q"], d["k"], d["v"], d["log_decay"])
+    cu = torch.tensor([0, T - 1, T - 1, T], dtype=torch.int32, device="cuda")
+    pool = torch.randn(4, 2, 64, 64, device="cuda")
+    before = pool.clone()
+    good = torch.tensor([2, -1, 0], dtype=torch.int32, device="cuda")
+    o = kda.la_chunk_forward_slots(*a, pool, good, cu)
+    after = pool.clone()
+    assert kda.device_status() == 0
+    for bad in (4, -2):
+        pool.copy_(before)
+        o2 = kda.la_chunk_forward_slots(*a, pool, torch.tensor([2, bad, 0], dtype=torch.int32, device="cuda"), cu)
+        assert kda.device_status() == kda.DEV_BAD_SLOT
+        assert torch.equal(o, o2) and torch.equal(pool, after)
+    assert kda.device_status() == 0
