@@ -117,8 +117,8 @@ __device__ __forceinline__ float rate_of(const float *log_decay, int h) {
 }
 
 // Flags entries of a slot table that are outside the pool: no span visits a packed sequence without
-// tokens.  A walk calls it with threads that have to wait for their first tiles anyway (not inlined: it costs
-// the loops behind it registers).
+// tokens.  The tensor-core walk calls it with threads that have to wait for their first tiles anyway (not inlined:
+// it costs the loops behind it registers; in the fp32 walk it cost 2 % even so, which has a launch of the join for it).
 __device__ __noinline__ void check_slots(int seqs, const int32_t *slots, int num_slots, int thread, int threads) {
     for (int n = blockIdx.x * threads + thread; n < seqs; n += gridDim.x * threads)
         if (slots[n] < -1 || slots[n] >= num_slots) flag_status(KDA_DEV_BAD_SLOT);

@@ -63,7 +63,6 @@ __global__ void __launch_bounds__(256) la_simt_kernel(Geo g, Walk wk, const floa
     const long long lo = g.lo(w), hi = g.hi(w);
     const long long E = DAB * DC;
     const Carry &y = wk.y;
-    if (WALK && DIR > 0 && g.cu && slots) check_slots(g.N, slots, num_slots, tid, 256);
 
     float S[RM][CG * 4];
     int head = -1;
@@ -346,10 +345,11 @@ cudaError_t launch_join(const Geo &g, const Call &c, int E, bool finals, const C
     return launch_after(la_join_kernel<C>, grid, 256, 0, c.st, g, j, c.log_decay, E, c.slots, c.num_slots);
 }
 
-// Where nothing is cut the join has only empty packed sequences' states to hand through.
+// Where nothing is cut the join has only empty packed sequences' states to hand through, and their
+// entries of a slot table to check where the walk does not.
 template <int C>
-cudaError_t launch_empty(const Geo &g, const Carry &y, const Call &c, int E) {
-    if (!g.cu || !y.last || y.last == y.s0) return cudaSuccess;
+cudaError_t launch_empty(const Geo &g, const Carry &y, const Call &c, int E, bool check) {
+    if (!g.cu || !y.last || (y.last == y.s0 && !check)) return cudaSuccess;
     Geo none = g;
     none.W = 0;
     Joins j{};
@@ -385,7 +385,7 @@ cudaError_t simt_forward(const Call &c, const void *q, const void *k, const void
     if (cut) {
         if ((e = launch_simt<DK, DV, Tin, 1, false>(g, wk, c, false)) != cudaSuccess) return e;
         if ((e = launch_join<kSimtC>(g, c, DK * DV, false, wk.y, 1)) != cudaSuccess) return e;
-    } else if ((e = launch_empty<kSimtC>(g, wk.y, c, DK * DV)) != cudaSuccess) {
+    } else if ((e = launch_empty<kSimtC>(g, wk.y, c, DK * DV, c.slots != nullptr)) != cudaSuccess) {
         return e;
     }
     return launch_simt<DK, DV, Tin, 1, true>(g, wk, c, cut);
@@ -408,7 +408,7 @@ cudaError_t simt_backward(const Call &c, const void *q, const void *k, const voi
         if ((e = launch_simt<DK, DV, Tin, 1, false>(g, sum_f, c, false)) != cudaSuccess) return e;
         if ((e = launch_simt<DK, DV, Tin, -1, false>(g, sum_b, c)) != cudaSuccess) return e;
         if ((e = launch_join<kSimtC>(g, c, E, false, fwd, 1, &bwd)) != cudaSuccess) return e;
-    } else if ((e = launch_empty<kSimtC>(g, bwd, c, E)) != cudaSuccess) {
+    } else if ((e = launch_empty<kSimtC>(g, bwd, c, E, false)) != cudaSuccess) {
         return e;
     }
     Carry bwd_t = bwd;

@@ -1057,7 +1057,7 @@ cudaError_t tc_forward(const Call &c, const void *q, const void *k, const void *
         a.role[0] = SumRole{tk, tv, y.sum_in, y.sum_out, 1, 1, last != nullptr};
         if ((e = launch_sum<DK, DV>(g, a, 1, c)) != cudaSuccess) return e;
         if ((e = launch_join<kC>(g, c, DK * DV, true, y, 1)) != cudaSuccess) return e;
-    } else if ((e = launch_empty<kC>(g, y, c, DK * DV)) != cudaSuccess) {
+    } else if ((e = launch_empty<kC>(g, y, c, DK * DV, false)) != cudaSuccess) {
         return e;
     }
     WalkArgs a{};
@@ -1086,7 +1086,7 @@ cudaError_t tc_backward(const Call &c, const void *q, const void *k, const void 
         a.role[1] = SumRole{tq, td, bwd.sum_in, bwd.sum_out, -1, 1, dinit != nullptr};
         if ((e = launch_sum<DK, DV>(g, a, 2, c)) != cudaSuccess) return e;
         if ((e = launch_join<kC>(g, c, E, true, fwd, 1, &bwd)) != cudaSuccess) return e;
-    } else if ((e = launch_empty<kC>(g, bwd, c, E)) != cudaSuccess) {
+    } else if ((e = launch_empty<kC>(g, bwd, c, E, false)) != cudaSuccess) {
         return e;
     }
     Carry bwd_t = bwd;
