@@ -418,6 +418,8 @@ struct PosGeo {
     int cvecs;              // C / VEC
     int tpr;                // threads of one row: min(cvecs, 256); a CTA holds 256 / tpr rows at a time
     int Z;                  // channel blocks: ceil(cvecs / tpr)
+    int span;               // channels of a block: tpr VEC
+    int ZG;                 // channel blocks that a group can touch
     __device__ __forceinline__ int rows_of(int tile) const { return min(tile_rows, L - tile * tile_rows); }
 };
 
@@ -437,9 +439,13 @@ __device__ __forceinline__ int channels_in(const PosGeo &p, int z, int g) {
     const Block<VEC> b(p, z);
     return min(b.c1, (g + 1) * p.D) - max(b.c0, g * p.D);
 }
-// Partial of (n, g, tile, z)
+// First block of group g, and the blocks that it touches
+__device__ __forceinline__ int first_block(const PosGeo &p, int g) { return g * p.D / p.span; }
+__device__ __forceinline__ int blocks_of(const PosGeo &p, int g) { return ((g + 1) * p.D - 1) / p.span - first_block(p, g) + 1; }
+// Partial of (n, g, tile, z): a group has places for its own blocks only (for all blocks the
+// workspace would grow with C^2 where groups are narrow)
 __device__ __forceinline__ long long part_at(const PosGeo &p, int n, int g, int tile, int z) {
-    return (((long long)n * p.G + g) * p.tiles + tile) * p.Z + z;
+    return (((long long)n * p.G + g) * p.tiles + tile) * p.ZG + (z - first_block(p, g));
 }
 
 // Lanes that work on one of `groups` groups: all 256 threads are busy with as many at once as fit a warp's shuffles.
@@ -551,7 +557,7 @@ __global__ void __launch_bounds__(kThreads) pos_apply_kernel(PosGeo p, const T *
     const int lanes = lanes_for(b.g1 - b.g0 + 1), sl = threadIdx.x & (lanes - 1);
     for (int g0 = b.g0 + (int)(threadIdx.x & ~31) / lanes; g0 <= b.g1; g0 += kThreads / lanes) {
         const int g = min(g0 + (int)(threadIdx.x & 31) / lanes, b.g1);
-        const int z0 = g * p.D / (p.tpr * VEC), zn = ((g + 1) * p.D - 1) / (p.tpr * VEC) - z0 + 1;
+        const int z0 = first_block(p, g), zn = blocks_of(p, g);
         const float inv = 1.f / ((float)p.L * p.D);
         const float2 v = pooled_moments(lanes, inv, [&](auto &&f) {
             for (int zz = z0; zz < z0 + zn; ++zz) {
@@ -559,7 +565,7 @@ __global__ void __launch_bounds__(kThreads) pos_apply_kernel(PosGeo p, const T *
                 const float2 *at = part + part_at(p, n, g, 0, zz);
 #pragma unroll 4
                 for (int t = sl; t < p.tiles; t += lanes) {
-                    const float2 u = at[(long long)t * p.Z];
+                    const float2 u = at[(long long)t * p.ZG];
                     f(w * p.rows_of(t), u.x, u.y);
                 }
             }
@@ -748,13 +754,13 @@ __global__ void __launch_bounds__(kThreads) pos_back_apply_kernel(
     const int lanes = lanes_for(b.g1 - b.g0 + 1), sl = threadIdx.x & (lanes - 1);
     for (int g0 = b.g0 + (int)(threadIdx.x & ~31) / lanes; g0 <= b.g1; g0 += kThreads / lanes) {
         const int g = min(g0 + (int)(threadIdx.x & 31) / lanes, b.g1);
-        const int z0 = g * p.D / (p.tpr * VEC), zn = ((g + 1) * p.D - 1) / (p.tpr * VEC) - z0 + 1;
+        const int z0 = first_block(p, g), zn = blocks_of(p, g);
         float s1 = 0.f, s2 = 0.f;
         for (int zz = z0; zz < z0 + zn; ++zz) {
             const float2 *at = part + part_at(p, n, g, 0, zz);
 #pragma unroll 4
             for (int t = sl; t < p.tiles; t += lanes) {
-                const float2 v = at[(long long)t * p.Z];
+                const float2 v = at[(long long)t * p.ZG];
                 s1 += v.x;
                 s2 += v.y;
             }
@@ -1242,12 +1248,14 @@ inline Plan plan_of(long long N, int L, int C, int G, int esize, bool gated, boo
     p.cvecs = s.vec ? C / vw : C;
     p.tpr = std::min(p.cvecs, kThreads);
     p.Z = (p.cvecs + p.tpr - 1) / p.tpr;
+    p.span = p.tpr * (s.vec ? vw : 1);
+    p.ZG = std::min(p.Z, (D + p.span - 2) / p.span + 1);
     const int rows = kThreads / p.tpr;                       // rows a CTA holds at a time
     const long long want = std::max<long long>(1, 2 * kSMs / (N * p.Z));   // tiles of a sample: two CTAs per SM
     const long long tr = std::max<long long>((L + want - 1) / want, (long long)8 * rows);
     p.tile_rows = (int)std::min<long long>(tr, L);
     p.tiles = (L + p.tile_rows - 1) / p.tile_rows;
-    const size_t group = (size_t)N * G * p.tiles * p.Z * sizeof(float2);
+    const size_t group = (size_t)N * G * p.tiles * p.ZG * sizeof(float2);
     s.ws = group + (backward ? (size_t)N * p.tiles * C * sizeof(float2) : 0);
     return s;
 }
@@ -1356,7 +1364,7 @@ cudaError_t launch_backward(const Plan &s, const Args &a, cudaStream_t st) {
     const long long tiles = (long long)s.p.N * s.p.tiles;
     const dim3 grid((unsigned)tiles, s.p.Z);
     const unsigned join = a.dweight || a.dbias ? (s.p.C + 31) / 32 : 0;
-    float2 *part = (float2 *)a.ws, *chan = part + (size_t)s.p.N * s.p.G * s.p.tiles * s.p.Z;
+    float2 *part = (float2 *)a.ws, *chan = part + (size_t)s.p.N * s.p.G * s.p.tiles * s.p.ZG;
     auto run = [&](auto sums, auto apply) {
         sums<<<grid, kThreads, 0, st>>>(s.p, dy, x, a.mean, a.rstd, a.weight, a.bias, gate, dgate, chan, part);
         const cudaError_t e = cudaGetLastError();

@@ -53,3 +53,44 @@ def test_host_threads_with_tiles_of_different_sizes():
         y, mean, rstd = kda.group_norm(t["x"], G)
         g = kda.group_norm_backward(t["dy"], t["x"], mean, rstd, G)
         assert torch.equal(y, t["y"]) and torch.equal(mean, t["mean"]) and torch.equal(g["dx"], t["dx"])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("shape,G", [((2, 1, 5003), 5003), ((1, 37, 5001), 1667), ((3, 2, 4099), 4099), ((2, 3, 3015), 3),
+                                     ((1, 21, 6007), 1), ((2, 50, 2304), 768), ((1, 3, 513), 27), ((1, 600, 1), 1)])
+def test_partial_sums_of_many_channel_blocks(dtype, shape, G):
+    """Groups inside one block of channels, across a border and over many blocks, in a workspace of exactly
+    the size that is asked for, with what lies behind it unchanged."""
+    N, L, C = shape
+    t = _tensors(shape, G, dtype, seed=C)
+    got = []
+    for backward in (False, True):
+        need = kda.group_norm_workspace_size(N, L, C, G, dtype, backward=backward)
+        room = torch.full((need + 4096,), 171, dtype=torch.uint8, device="cuda")
+        ws = room[:need] if need else None
+        if not backward:
+            y, mean, rstd = kda.group_norm(t["x"], G, activation="none", workspace=ws)
+            got.append(y)
+        else:
+            w = torch.ones(C, device="cuda")
+            g = kda.group_norm_backward(t["dy"], t["x"], mean, rstd, G, w, w * 0, activation="none", workspace=ws)
+        torch.cuda.synchronize()
+        assert (room[need:] == 171).all()
+    x = t["x"].double().requires_grad_()
+    h = x.reshape(N, L, G, C // G)
+    m, v = h.mean(dim=(1, 3), keepdim=True), h.var(dim=(1, 3), unbiased=False, keepdim=True)
+    want = ((h - m) * (v + 1e-5).rsqrt()).reshape(shape)
+    want.backward(t["dy"].double())
+    # fp32 sums of n values around a mean of 0, in the root mean square; a group of one or two values may be
+    # divided by a deviation far below the values (or by eps), which multiplies the mean's error
+    n = L * C // G
+    scale = 1 + float(((v + 1e-5).rsqrt() * h.abs().amax(dim=(1, 3), keepdim=True)).max().detach())
+    tol = scale * 2.0 ** -24 * (n + 32) ** 0.5 * 8 + (2.0 ** -8 if dtype == BF16 else 0)
+    size = float(want.detach().norm()) + 2.0 ** -10
+    assert float((y.double() - want.detach()).norm()) <= tol * size
+    assert float((g["dx"].double() - x.grad).norm()) <= tol * scale * (float(x.grad.norm()) + 2.0 ** -10 * float(t["dy"].double().norm()))
+    assert float((mean.double() - m.detach().view(N, G)).abs().max()) <= 2.0 ** -24 * (n + 32) * float(h.detach().abs().max())
+    xhat = want.detach()
+    dw, db = (t["dy"].double() * xhat).sum((0, 1)), t["dy"].double().sum((0, 1))
+    assert float((g["dweight"].double() - dw).norm()) <= 2 * tol * (float(dw.norm()) + 2.0 ** -10 * float(t["dy"].double().norm()))
+    assert float((g["dbias"].double() - db).norm()) <= 2.0 ** -22 * (N * L + 32) ** 0.5 * float(t["dy"].double().norm())

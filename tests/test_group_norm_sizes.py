@@ -1,0 +1,16 @@
+"""Workspace sizes of group norm (CPU: the library only computes them)."""
+import pytest
+import torch
+
+import gated_delta_rule_85_b200 as kda
+
+
+@pytest.mark.parametrize("C,G", [(65537, 65537), (262147, 262147), (1000003, 1000003), (999999, 333333), (16776959, 16776959)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N,L", [(1, 1), (3, 1), (1, 40)])
+def test_narrow_groups_take_a_multiple_of_the_tensor(C, G, dtype, N, L):
+    """One partial sum (8 bytes) for each group, row tile and one or two channel blocks; gradients add one
+    for each channel and row tile.  A row tile is at least 8 positions, or the sample's."""
+    tiles = N * -(-L // min(L, 8))
+    assert kda.group_norm_workspace_size(N, L, C, G, dtype) <= 2 * 8 * G * tiles
+    assert kda.group_norm_workspace_size(N, L, C, G, dtype, backward=True) <= 2 * 8 * G * tiles + 8 * C * tiles
