@@ -12,12 +12,19 @@ using namespace kda::host;
 
 namespace {
 
-// Shared checks of the prefill and its backward pass; `states` names two optional fp32 state tensors.
+constexpr ArgNames kForwardNames{"q, k, v, log_decay and o", "log_decay", "init_state", "o", "final_state"};
+constexpr ArgNames kPoolNames{"q, k, v, log_decay and o", "log_decay", "state_pool", "o", "state_pool"};
+constexpr ArgNames kBackwardNames{"q, k, v, log_decay and d_o", "log_decay", "init_state", "d_o", "dfinal_state"};
+constexpr ArgNames kStepNames{"q, k, v, log_decay, state and o", "log_decay", "state", "o", nullptr};
+constexpr ArgNames kPoolStepNames{"q, k, v, log_decay, state_pool and o", "log_decay", "state_pool", "o", nullptr};
+
+// Shared checks of the prefill and its backward pass: s0 and last are two optional fp32 state tensors.
 int check_la(const void *q, const void *k, const void *v, const float *log_decay, const float *s0, const void *o,
-             const float *last, const int32_t *cu_seqlens, int B, int T, int H, int dk, int dv, int num_seqs, int dtype) {
+             const float *last, const int32_t *cu_seqlens, int B, int T, int H, int dk, int dv, int num_seqs, int dtype,
+             const ArgNames &names) {
     // beta is not part of this operator: log_decay stands in (both are 4-byte aligned device arrays)
     int rc = check_prefill(q, k, v, log_decay, log_decay, s0, o, last, cu_seqlens, B, T, H, dk, dv, num_seqs, dtype, 64,
-                           true);
+                           true, names);
     if (rc) return rc;
     if ((long long)B * T > 0x7fffffffLL)
         return fail(KDA_ERR_UNSUPPORTED, "B*T=%lld exceeds 2^31 - 1 tokens", (long long)B * T);
@@ -87,7 +94,8 @@ int kda_la_chunk_forward(const void *q, const void *k, const void *v, const floa
                          const float *init_state, void *o, float *final_state, const int32_t *cu_seqlens, int B,
                          int T, int H, int dk, int dv, int num_seqs, int dtype, void *workspace, size_t ws_bytes,
                          void *stream) {
-    int rc = check_la(q, k, v, log_decay, init_state, o, final_state, cu_seqlens, B, T, H, dk, dv, num_seqs, dtype);
+    int rc = check_la(q, k, v, log_decay, init_state, o, final_state, cu_seqlens, B, T, H, dk, dv, num_seqs, dtype,
+                      kForwardNames);
     if (rc) return rc;
     rc = check_workspace(workspace, ws_bytes,
                          kda_la_chunk_forward_workspace_size(B, T, H, dk, dv, num_seqs, dtype, 0));
@@ -102,7 +110,8 @@ int kda_la_chunk_forward_slots(const void *q, const void *k, const void *v, cons
                                float *state_pool, const int32_t *slots, void *o, const int32_t *cu_seqlens, int B,
                                int T, int H, int dk, int dv, int num_seqs, int num_slots, int dtype,
                                void *workspace, size_t ws_bytes, void *stream) {
-    int rc = check_la(q, k, v, log_decay, state_pool, o, state_pool, cu_seqlens, B, T, H, dk, dv, num_seqs, dtype);
+    int rc = check_la(q, k, v, log_decay, state_pool, o, state_pool, cu_seqlens, B, T, H, dk, dv, num_seqs, dtype,
+                      kPoolNames);
     if (rc) return rc;
     if (num_seqs > 0 && (!state_pool || !slots))
         return fail(KDA_ERR_INVALID_ARG, "state_pool and slots are required");
@@ -117,7 +126,7 @@ int kda_la_chunk_forward_slots(const void *q, const void *k, const void *v, cons
 
 int kda_la_recurrent_step(const void *q, const void *k, const void *v, const float *log_decay, float *state, void *o,
                           int N, int H, int dk, int dv, int dtype, void *stream) {
-    int rc = check_decode(q, k, v, log_decay, log_decay, state, o, N, H, dk, dv, dtype, true);
+    int rc = check_decode(q, k, v, log_decay, log_decay, state, o, N, H, dk, dv, dtype, true, kStepNames);
     if (rc || N == 0) return rc;
     return la_step(q, k, v, log_decay, state, o, N, H, dk, dv, dtype, nullptr, 0, (cudaStream_t)stream);
 }
@@ -125,7 +134,7 @@ int kda_la_recurrent_step(const void *q, const void *k, const void *v, const flo
 int kda_la_recurrent_step_slots(const void *q, const void *k, const void *v, const float *log_decay,
                                 float *state_pool, const int32_t *slots, void *o, int N, int H, int dk, int dv,
                                 int num_slots, int dtype, void *stream) {
-    int rc = check_decode(q, k, v, log_decay, log_decay, state_pool, o, N, H, dk, dv, dtype, true);
+    int rc = check_decode(q, k, v, log_decay, log_decay, state_pool, o, N, H, dk, dv, dtype, true, kPoolStepNames);
     if (rc || N == 0) return rc;
     if (!slots) return fail(KDA_ERR_INVALID_ARG, "slots is required");
     if (!aligned(slots, 4)) return fail(KDA_ERR_MISALIGNED, "slots is not 4-byte aligned");
@@ -143,7 +152,8 @@ int kda_la_chunk_backward(const void *q, const void *k, const void *v, const flo
                           void *dk_out, void *dv_out, float *dinit_state, const int32_t *cu_seqlens, int B, int T,
                           int H, int dk, int dv, int num_seqs, int dtype, void *workspace, size_t ws_bytes,
                           void *stream) {
-    int rc = check_la(q, k, v, log_decay, init_state, d_o, dfinal_state, cu_seqlens, B, T, H, dk, dv, num_seqs, dtype);
+    int rc = check_la(q, k, v, log_decay, init_state, d_o, dfinal_state, cu_seqlens, B, T, H, dk, dv, num_seqs, dtype,
+                      kBackwardNames);
     if (rc) return rc;
     if (T > 0 && (!dq || !dk_out || !dv_out)) return fail(KDA_ERR_INVALID_ARG, "dq, dk and dv are required");
     const void *p16[] = {dq, dk_out, dv_out, dinit_state};

@@ -38,16 +38,16 @@ int cuda_fail(cudaError_t e, const char *what) {
     return fail(KDA_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
 }
 
-// Validation shared by both prefill entry points.
+// Validation shared by the prefill entry points.
 int check_prefill(const void *q, const void *k, const void *v, const float *log_alpha,
                   const float *beta, const float *init_state, const void *o, const float *final_state,
                   const int32_t *cu_seqlens, int B, int T, int H, int dk, int dv, int num_seqs,
-                  int dtype, int chunk, bool gate_scalar) {
+                  int dtype, int chunk, bool gate_scalar, const ArgNames &names) {
     if (B < 1 || T < 0 || H < 1 || num_seqs < 0)
         return fail(KDA_ERR_INVALID_ARG, "bad sizes B=%d T=%d H=%d num_seqs=%d", B, T, H, num_seqs);
     // With no tokens the per-token tensors are empty and may be NULL.
     if (T > 0 && (!q || !k || !v || !log_alpha || !beta || !o))
-        return fail(KDA_ERR_INVALID_ARG, "q, k, v, log_alpha, beta and o are required");
+        return fail(KDA_ERR_INVALID_ARG, "%s are required", names.required);
     if (H > 65535) return fail(KDA_ERR_UNSUPPORTED, "H=%d above 65535", H);
     if (cu_seqlens) {
         if (B != 1) return fail(KDA_ERR_INVALID_ARG, "packed (cu_seqlens) input needs B == 1, got %d", B);
@@ -61,28 +61,29 @@ int check_prefill(const void *q, const void *k, const void *v, const float *log_
     if (chunk != 64) return fail(KDA_ERR_UNSUPPORTED, "chunk=%d: only 64 is supported", chunk);
     if (dtype != KDA_BF16 && dtype != KDA_F32) return fail(KDA_ERR_UNSUPPORTED, "dtype=%d", dtype);
     const void *p16[] = {q, k, v, gate_scalar ? nullptr : log_alpha, o, init_state, final_state};
-    const char *n16[] = {"q", "k", "v", "log_alpha", "o", "init_state", "final_state"};
+    const char *n16[] = {"q", "k", "v", names.gate, names.o, names.init_state, names.final_state};
     for (int i = 0; i < 7; ++i)
         if (p16[i] && !aligned(p16[i], 16)) return fail(KDA_ERR_MISALIGNED, "%s is not 16-byte aligned", n16[i]);
     if (gate_scalar && log_alpha && !aligned(log_alpha, 4))
-        return fail(KDA_ERR_MISALIGNED, "log_alpha is not 4-byte aligned");
+        return fail(KDA_ERR_MISALIGNED, "%s is not 4-byte aligned", names.gate);
     if (beta && !aligned(beta, 4)) return fail(KDA_ERR_MISALIGNED, "beta is not 4-byte aligned");
     if (cu_seqlens && !aligned(cu_seqlens, 4)) return fail(KDA_ERR_MISALIGNED, "cu_seqlens is not 4-byte aligned");
     return KDA_OK;
 }
 
+// Argument checks shared by the decode entry points.
 int check_decode(const void *q, const void *k, const void *v, const float *log_alpha, const float *beta,
                  const float *state, const void *o, int N, int H, int dk, int dv, int dtype,
-                 bool gate_scalar) {
+                 bool gate_scalar, const ArgNames &names) {
     if (N < 0 || H < 1) return fail(KDA_ERR_INVALID_ARG, "bad sizes N=%d H=%d", N, H);
     if (N == 0) return KDA_OK;   // nothing to do; empty tensors may carry NULL pointers
     if (!q || !k || !v || !log_alpha || !beta || !state || !o)
-        return fail(KDA_ERR_INVALID_ARG, "q, k, v, log_alpha, beta, state and o are required");
+        return fail(KDA_ERR_INVALID_ARG, "%s are required", names.required);
     if ((dk != 64 && dk != 128) || (dv != 64 && dv != 128))
         return fail(KDA_ERR_UNSUPPORTED, "dk=%d dv=%d: each must be 64 or 128", dk, dv);
     if (dtype != KDA_BF16 && dtype != KDA_F32) return fail(KDA_ERR_UNSUPPORTED, "dtype=%d", dtype);
     const void *p16[] = {q, k, v, log_alpha, o, state};
-    const char *n16[] = {"q", "k", "v", "log_alpha", "o", "state"};
+    const char *n16[] = {"q", "k", "v", names.gate, names.o, names.init_state};
     for (int i = 0; i < 6; ++i)
         if (!aligned(p16[i], (i == 3 && gate_scalar) ? 4 : 16))
             return fail(KDA_ERR_MISALIGNED, "%s is not %d-byte aligned", n16[i], (i == 3 && gate_scalar) ? 4 : 16);
@@ -352,7 +353,7 @@ int prefill_impl(const void *q, const void *k, const void *v, const float *log_a
     return KDA_OK;
 }
 
-// Decode argument checks shared by both decode entry points.
+// Launches the decode kernel of these sizes and types.
 int decode_impl(const void *q, const void *k, const void *v, const float *log_alpha, const float *beta,
                 float *state, void *o, int N, int H, int dk, int dv, int dtype, const int32_t *slots,
                 int num_slots, bool gate_scalar, cudaStream_t st, bool prologue = false) {
