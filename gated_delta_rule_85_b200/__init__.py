@@ -562,7 +562,14 @@ def _on_device(dev, **tensors):
             raise ValueError(f"{name} must be contiguous in the documented layout")
 
 
+def _require(**tensors):
+    for name, t in tensors.items():
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} is required, a tensor")
+
+
 def _expect(name, t, shape, dtype):
+    """An optional tensor (None: not given) has this shape and type."""
     if t is not None and (t.shape != shape or t.dtype != dtype):
         raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
 
@@ -679,6 +686,7 @@ def la_chunk_forward(q, k, v, log_decay, init_state=None, cu_seqlens=None, *, o=
     r = (_fast or _load_fast()).la_forward(q, k, v, log_decay, init_state, cu_seqlens, o, final_state, workspace)
     if r is not None:
         return _done(r)
+    _require(q=q, k=k, v=v, log_decay=log_decay)
     B, T, H, dk, dv, N, dt = _la_shapes(q, k, v, log_decay, cu_seqlens)
     state = (N, H, dk, dv)
     if init_state is not None:
@@ -710,6 +718,7 @@ def la_chunk_forward_slots(q, k, v, log_decay, state_pool, slots, cu_seqlens=Non
     r = (_fast or _load_fast()).la_forward_slots(q, k, v, log_decay, state_pool, slots, cu_seqlens, o, workspace)
     if r is not None:
         return _done(r)
+    _require(q=q, k=k, v=v, log_decay=log_decay, state_pool=state_pool, slots=slots)
     B, T, H, dk, dv, N, dt = _la_shapes(q, k, v, log_decay, cu_seqlens)
     _expect("state_pool", state_pool, (*state_pool.shape[:1], H, dk, dv), torch.float32)
     _expect("slots", slots, (N,), torch.int32)
@@ -742,6 +751,7 @@ def la_chunk_backward(q, k, v, log_decay, d_o, init_state=None, dfinal_state=Non
                                                 dinit_state, workspace)
         if r is not None:
             return _done(r)
+    _require(q=q, k=k, v=v, log_decay=log_decay, d_o=d_o)
     B, T, H, dk, dv, N, dt = _la_shapes(q, k, v, log_decay, cu_seqlens)
     dev = q.device
     state = (N, H, dk, dv)
@@ -798,6 +808,7 @@ def la_recurrent_step(q, k, v, log_decay, state, o=None):
     r = (_fast or _load_fast()).la_step(q, k, v, log_decay, state, None, o)
     if r is not None:
         return _done(r)
+    _require(q=q, k=k, v=v, log_decay=log_decay, state=state)
     N, H, dk, dv, dt, o = _la_step_shapes(q, k, v, log_decay, "state", state, 0, o)
     index = q.get_device()
     if not _placed(index, (q, k, v, log_decay, state, o)):
@@ -813,6 +824,7 @@ def la_recurrent_step_slots(q, k, v, log_decay, state_pool, slots, o=None):
     r = (_fast or _load_fast()).la_step(q, k, v, log_decay, state_pool, slots, o) if slots is not None else None
     if r is not None:
         return _done(r)
+    _require(q=q, k=k, v=v, log_decay=log_decay, state_pool=state_pool, slots=slots)
     N, H, dk, dv, dt, o = _la_step_shapes(q, k, v, log_decay, "state_pool", state_pool, None, o)
     _expect("slots", slots, (N,), torch.int32)
     index = q.get_device()
@@ -870,6 +882,7 @@ def group_norm(x, num_groups, weight=None, bias=None, gate=None, *, eps=1e-5, ac
     r = (_fast or _load_fast()).norm(x, num_groups, weight, bias, gate, eps, ACTIVATIONS.get(activation), y, workspace)
     if r is not None:
         return _done(r)
+    _require(x=x)
     N, L, C, dt, act = _norm_shapes(x, num_groups, weight, bias, gate, activation)
     if not eps > 0:
         raise ValueError(f"eps must be above 0, got {eps}")
@@ -898,6 +911,7 @@ def group_norm_backward(dy, x, mean, rstd, num_groups, weight=None, bias=None, g
                                                   ACTIVATIONS.get(activation), workspace)
         if r is not None:
             return _done(r)
+    _require(dy=dy, x=x, mean=mean, rstd=rstd)
     N, L, C, dt, act = _norm_shapes(x, num_groups, weight, bias, gate, activation)
     dev = x.device
     _expect("dy", dy, x.shape, x.dtype)
