@@ -22,6 +22,8 @@ import ctypes
 import functools
 import importlib.util
 import os
+import sys
+import warnings
 from types import SimpleNamespace
 
 import torch
@@ -578,17 +580,35 @@ def _expect(name, t, shape, dtype):
 # short way (csrc/kda_fast.cpp), which makes the same checks and answers None where one does not
 # hold; what it leaves (a call to refuse, another device's tensors, given gradients) goes on here.
 
+class _LongWay:
+    """In the short way's place where it cannot be used: leaves every call to Python."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def _load_fast():
-    """The compiled short way (built with libkda.so); raise if absent."""
+    """The compiled short way, built with libkda.so for one torch and Python.  Where it is missing or was
+    built for others the calls run without it, each a few microseconds slower; a warning says so once."""
     global _fast
     if _fast is None:
         load_library()
         path = os.path.join(_HERE, "_kda_fast.so")
+        why = None
         if not os.path.exists(path):
-            raise RuntimeError(f"_kda_fast.so is not built ({path}); run gated_delta_rule_85_b200/build.py")
-        spec = importlib.util.spec_from_file_location("_kda_fast", path)
-        _fast = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(_fast)
+            why = f"is not built ({path})"
+        else:
+            try:
+                spec = importlib.util.spec_from_file_location("_kda_fast", path)
+                fast = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(fast)
+                if fast.built_for != f"torch {torch.__version__}, python {sys.version_info[0]}.{sys.version_info[1]}":
+                    why = f"was built for {fast.built_for}"
+            except ImportError as e:
+                why = f"does not load ({e})"
+        if why:
+            warnings.warn(f"_kda_fast.so {why}; small calls take longer until gated_delta_rule_85_b200/build.py runs")
+        _fast = _LongWay() if why else fast
     return _fast
 
 

@@ -52,6 +52,22 @@ def _sources(unit: str):
     return [os.path.join(HERE, "csrc", f) for f in [unit, *UNITS[unit]]] + [os.path.join(ROOT, "include", "kda.h")]
 
 
+def _built_for() -> str:
+    """What _kda_fast.so depends on beside its sources."""
+    import sys
+
+    import torch
+
+    return f"torch {torch.__version__}, python {sys.version_info[0]}.{sys.version_info[1]}"
+
+
+def _fast_stale(sources) -> bool:
+    if _newer(FAST, sources):
+        return True
+    with open(FAST, "rb") as f:
+        return _built_for().encode() + b"\0" not in f.read()
+
+
 def _fast_command(out: str):
     import sysconfig
 
@@ -62,7 +78,7 @@ def _fast_command(out: str):
     includes = [*ext.include_paths(), sysconfig.get_paths()["include"],
                 os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
     return [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
-            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-isystem{i}" for i in includes],
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DKDA_BUILT_FOR="{_built_for()}"', *[f"-isystem{i}" for i in includes],
             "-o", out, os.path.join(HERE, "csrc", "kda_fast.cpp"), "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
             "-L", HERE, "-l:libkda.so", "-Wl,-rpath,$ORIGIN"]
 
@@ -70,7 +86,7 @@ def _fast_command(out: str):
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     fast_sources = [os.path.join(HERE, "csrc", "kda_fast.cpp"), os.path.join(ROOT, "include", "kda.h")]
     stale = force or _newer(LIB, [f for u in UNITS for f in _sources(u)])
-    if not stale and not _newer(FAST, fast_sources):
+    if not stale and not _fast_stale(fast_sources):
         return LIB
     tag = f".tmp{os.getpid()}"
 
@@ -95,7 +111,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
              for unit in UNITS if force or _newer(_object(unit), _sources(unit))])
         run([([cc, *NVCC_FLAGS[:2], "-shared", "-Xlinker", "-soname=libkda.so", "-o", LIB + tag,
                *[_object(u) for u in UNITS]], LIB)])
-    if force or _newer(FAST, fast_sources):
+    if force or _fast_stale(fast_sources):
         run([(_fast_command(FAST + tag), FAST)])
     return LIB
 

@@ -331,4 +331,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kda_fast", nullptr, -1, methods, 
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__kda_fast() { return PyModule_Create(&module); }
+// KDA_BUILT_FOR: the torch and Python whose headers this was compiled with; the binding uses it with no others.
+PyMODINIT_FUNC PyInit__kda_fast() {
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", KDA_BUILT_FOR) != 0) Py_CLEAR(m);
+    return m;
+}

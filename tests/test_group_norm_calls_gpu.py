@@ -94,3 +94,42 @@ def test_partial_sums_of_many_channel_blocks(dtype, shape, G):
     dw, db = (t["dy"].double() * xhat).sum((0, 1)), t["dy"].double().sum((0, 1))
     assert float((g["dweight"].double() - dw).norm()) <= 2 * tol * (float(dw.norm()) + 2.0 ** -10 * float(t["dy"].double().norm()))
     assert float((g["dbias"].double() - db).norm()) <= 2.0 ** -22 * (N * L + 32) ** 0.5 * float(t["dy"].double().norm())
+
+
+@pytest.mark.parametrize("shape,G", [((5, 4 * 128), 4), ((2, 70, 48), 6), ((2, 7 * 13), 7)])
+@pytest.mark.parametrize("gate", [False, True])
+def test_either_way(monkeypatch, shape, G, gate):
+    """The compiled short way and the Python way give the same bits and make the same refusals."""
+    t = _tensors(shape, G, BF16, seed=9)
+    C = shape[-1]
+    w, b = torch.linspace(0.5, 1.5, C, device="cuda"), torch.linspace(-1, 1, C, device="cuda")
+    ga = t["dy"].flip(0).contiguous() if gate else None
+    odd = torch.empty(t["x"].numel() + 1, dtype=BF16, device="cuda")[1:].view(shape)
+    got = []
+    for long_way in (False, True):
+        if long_way:
+            monkeypatch.setattr(kda, "_fast", kda._LongWay())
+        y, mean, rstd = kda.group_norm(t["x"], G, w, b, ga, eps=1e-4)
+        g = kda.group_norm_backward(t["dy"], t["x"], mean, rstd, G, w, b, ga)
+        plain = kda.group_norm(t["x"], G, activation="none")
+        got.append((y, mean, rstd, *(g[k] for k in sorted(g)), *plain))
+        given = torch.full_like(t["x"], 7.0)
+        assert kda.group_norm(t["x"], G, w, b, ga, eps=1e-4, y=given)[0] is given and torch.equal(given, y)
+        with pytest.raises(kda.KDAError, match="aligned"):
+            kda.group_norm(odd, G)
+        with pytest.raises(ValueError, match="eps"):
+            kda.group_norm(t["x"], G, eps=-1.0)
+        with pytest.raises(ValueError, match="activation"):
+            kda.group_norm(t["x"], G, activation="relu")
+        with pytest.raises(ValueError, match="groups"):
+            kda.group_norm(t["x"], C + 1)
+        with pytest.raises(ValueError, match="weight must be"):
+            kda.group_norm(t["x"], G, w.double())
+        with pytest.raises(ValueError, match="is on cpu"):
+            kda.group_norm_backward(t["dy"], t["x"], mean.cpu(), rstd, G)
+        with pytest.raises(ValueError, match="dy is required"):
+            kda.group_norm_backward(None, t["x"], mean, rstd, G)
+        with pytest.raises(TypeError):
+            kda.group_norm(t["x"].half(), G)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(*got))

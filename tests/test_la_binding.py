@@ -1,4 +1,6 @@
 """The Python binding of linear attention and group norm: what it does without a GPU."""
+import os
+
 import pytest
 import torch
 
@@ -36,3 +38,31 @@ def test_required_tensors_are_named(call):
             bad[i] = other
             with pytest.raises(ValueError, match=f"{name} is required"):
                 getattr(kda, call)(*bad)
+
+
+@pytest.mark.parametrize("case", ["missing", "another torch", "no library"])
+def test_calls_go_on_without_the_short_way(case, monkeypatch, tmp_path):
+    kda.load_library()
+    monkeypatch.setattr(kda, "_fast", None)
+    if case == "another torch":
+        monkeypatch.setattr(torch, "__version__", "0.0")
+    else:
+        monkeypatch.setattr(kda, "_HERE", str(tmp_path))
+    if case == "no library":
+        (tmp_path / "_kda_fast.so").write_bytes(b"not a library")
+    with pytest.warns(UserWarning, match="_kda_fast.so"):
+        with pytest.raises(ValueError, match="CUDA"):
+            kda.la_chunk_forward(Q, Q, Q, LG)
+    for call, (args, _) in CALLS.items():   # no second warning, and every call by its Python way
+        with pytest.raises(ValueError, match="CUDA"):
+            getattr(kda, call)(*args)
+
+
+def test_short_way_is_built_again_for_another_torch(monkeypatch):
+    from gated_delta_rule_85_b200 import build
+
+    sources = [os.path.join(build.HERE, "csrc", "kda_fast.cpp")]
+    assert not build._fast_stale(sources)
+    assert kda._load_fast().built_for == build._built_for()
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + ".1")
+    assert build._fast_stale(sources)
