@@ -33,7 +33,8 @@ int check_decode(const void *q, const void *k, const void *v, const float *log_a
                  const ArgNames &names = kDeltaStepNames);
 int check_workspace(const void *workspace, size_t ws_bytes, size_t need);
 
-// A unit's device status word, for kda_get_device_status.
+// A unit's device status word, for kda_get_device_status; at most kStatusUnits units have one.
+constexpr int kStatusUnits = 4;
 struct StatusWord {
     const void *symbol;
     StatusWord *next;

@@ -520,6 +520,16 @@ __global__ void wait_timeout_kernel(long long limit_cycles) {
     const bool ok = ptx::mbar_wait_bounded(addr, 0u, limit_cycles);
     if (__syncthreads_or(!ok) && threadIdx.x == 0) flag_status(KDA_DEV_WAIT_TIMEOUT);
 }
+
+// Status words of the other units, and the kernel that moves their flags into this unit's word.
+struct StatusWords {
+    unsigned int *at[host::kStatusUnits];
+    int n;
+};
+__global__ void gather_status_kernel(StatusWords words) {
+    for (int i = 0; i < words.n; ++i)
+        if (*words.at[i]) flag_status(atomicExch(words.at[i], 0u));
+}
 }  // namespace kda
 
 extern "C" {
@@ -781,19 +791,25 @@ int kda_debug_wait_timeout(long long limit_cycles, void *stream) {
 int kda_get_device_status(unsigned int *bits, int clear, void *stream) {
     if (!bits) return fail(KDA_ERR_INVALID_ARG, "bits is required");
     cudaStream_t st = (cudaStream_t)stream;
+    // one copy and one wait, however many units there are: their words are first moved into this unit's
+    kda::StatusWords others{};
+    cudaError_t e = cudaSuccess;
+    for (const StatusWord *w = kda::host::g_words; w && e == cudaSuccess; w = w->next)
+        if (w->symbol != &kda::g_status && others.n < kStatusUnits)
+            e = cudaGetSymbolAddress((void **)&others.at[others.n++], w->symbol);
+    if (others.n && e == cudaSuccess) {
+        kda::gather_status_kernel<<<1, 1, 0, st>>>(others);
+        e = cudaGetLastError();
+    }
     unsigned int all = 0;
-    for (const StatusWord *w = kda::host::g_words; w; w = w->next) {
-        unsigned int host = 0;
-        cudaError_t e = cudaMemcpyFromSymbolAsync(&host, w->symbol, sizeof(host), 0, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(&all, kda::g_status, sizeof(all), 0, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e != cudaSuccess) return cuda_fail(e, "reading the device status word");
+    if (clear && all) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbolAsync(kda::g_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st);
         if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-        if (e != cudaSuccess) return cuda_fail(e, "reading the device status word");
-        if (clear && host) {
-            const unsigned int zero = 0;
-            e = cudaMemcpyToSymbolAsync(w->symbol, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st);
-            if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-            if (e != cudaSuccess) return cuda_fail(e, "clearing the device status word");
-        }
-        all |= host;
+        if (e != cudaSuccess) return cuda_fail(e, "clearing the device status word");
     }
     *bits = all;
     if (all) return fail(KDA_ERR_DEVICE, "device status flags 0x%x", all);
