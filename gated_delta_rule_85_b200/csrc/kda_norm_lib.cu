@@ -6,6 +6,10 @@ using namespace kda::host;
 
 namespace {
 
+// 65535 blocks of 256 channels; samples and groups that a grid and 32-bit counts hold.
+constexpr int kMaxC = 65535 * 256, kMaxL = 1 << 30;
+constexpr long long kMaxN = 1LL << 24, kMaxGroups = 1LL << 30;
+
 int check_norm(const void *x, const void *y, const float *mean, const float *rstd, const float *weight,
                const float *bias, const void *gate, long long N, int L, int C, int G, int act, int dtype) {
     if (N < 0 || L < 1 || C < 1 || G < 1) return fail(KDA_ERR_INVALID_ARG, "bad sizes N=%lld L=%d C=%d G=%d", N, L, C, G);
@@ -13,9 +17,8 @@ int check_norm(const void *x, const void *y, const float *mean, const float *rst
     if (act != KDA_ACT_NONE && act != KDA_ACT_SILU && act != KDA_ACT_SIGMOID)
         return fail(KDA_ERR_INVALID_ARG, "act=%d is not a KDA_ACT_* value", act);
     if (dtype != KDA_BF16 && dtype != KDA_F32) return fail(KDA_ERR_UNSUPPORTED, "dtype=%d", dtype);
-    if (C > 65535 * 256 || L > (1 << 30))   // (65535 blocks of 256 channels)
-        return fail(KDA_ERR_UNSUPPORTED, "C=%d above 16776960 or L=%d above 2^30", C, L);
-    if (N > (1LL << 31) / G / 2 || N > 1LL << 24)
+    if (C > kMaxC || L > kMaxL) return fail(KDA_ERR_UNSUPPORTED, "C=%d above 16776960 or L=%d above 2^30", C, L);
+    if (N > kMaxN || N > kMaxGroups / G)
         return fail(KDA_ERR_UNSUPPORTED, "N=%lld with G=%d: at most 2^24 samples and 2^30 groups", N, G);
     if (N == 0) return KDA_OK;
     if (!x || !y || !mean || !rstd) return fail(KDA_ERR_INVALID_ARG, "x, mean, rstd and the outputs are required");
@@ -35,6 +38,7 @@ extern "C" {
 
 size_t kda_group_norm_workspace_size(long long N, int L, int C, int G, int dtype, int backward) {
     if (N < 1 || L < 1 || C < 1 || G < 1 || C % G || (dtype != KDA_BF16 && dtype != KDA_F32)) return 0;
+    if (C > kMaxC || L > kMaxL || N > kMaxN || N > kMaxGroups / G) return 0;   // the calls refuse these
     // (with and without a gate: the forms may differ)
     const int es = dtype == KDA_BF16 ? 2 : 4;
     return std::max(kda::norm::plan_of(N, L, C, G, es, false, backward != 0).ws,

@@ -521,7 +521,9 @@ int kda_la_chunk_backward(const void *q, const void *k, const void *v, const flo
  *   mean, rstd    fp32 [N, G], written (the backward call reads them)
  *   act           KDA_ACT_*;  eps > 0;  C a multiple of G
  *   workspace     kda_group_norm_workspace_size() bytes, 256-byte aligned (0: may be NULL)
- * N = 0 is a no-op.  Statistics and arithmetic are fp32, y is rounded once.
+ * N = 0 is a no-op.  Statistics and arithmetic are fp32, y is rounded once.  At most 2^24
+ * samples, 2^30 groups (N G), 2^30 positions and 16776960 channels; more is
+ * KDA_ERR_UNSUPPORTED, and the workspace size of what is refused is 0.
  */
 #define KDA_ACT_NONE 0
 #define KDA_ACT_SILU 1
