@@ -32,7 +32,8 @@ int check_la(const void *q, const void *k, const void *v, const float *log_decay
 }
 
 bool la_sizes_ok(int B, int T, int H, int dk, int dv, int num_seqs, int dtype) {
-    return B >= 1 && T >= 0 && H >= 1 && num_seqs >= 0 && (dk == 64 || dk == 128) && (dv == 64 || dv == 128) &&
+    return B >= 1 && T >= 0 && H >= 1 && H <= 65535 && num_seqs >= 0 && num_seqs <= 65535 &&
+           (long long)B * T <= 0x7fffffffLL && (dk == 64 || dk == 128) && (dv == 64 || dv == 128) &&
            (dtype == KDA_BF16 || dtype == KDA_F32);
 }
 

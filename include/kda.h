@@ -451,6 +451,8 @@ int kda_gdn_chunk_backward_ex(const void *q, const void *k, const void *v, const
  *   workspace     kda_la_chunk_forward_workspace_size() bytes, 256-byte aligned
  *                 (30 MB at most plus, with slots, one state per sequence and head,
  *                 whatever T); calls that can overlap in time need their own
+ * B T is at most 2^31 - 1 tokens; H and num_seqs at most 65535.  The workspace size of
+ * what is refused is 0.
  * KDA_BF16 runs on the tensor cores with fp32 accumulation, and final_state keeps fp32
  * accuracy.  On the way to o (and to dq, dk, dv) the decayed scores and the state that a
  * chunk's rows read are rounded to bf16 once each, as operands; the powers of the decay

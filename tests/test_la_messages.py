@@ -38,3 +38,14 @@ def test_delta_rule_names_stay(lib):  # noqa: F811
     assert "log_alpha, beta, state and o are required" in lib.kda_last_error().decode()
     assert f(A[0], A[1], A[2], A[3] + 4, A[4], A[5], A[6], 4, 2, 64, 64, 0, None) != 0
     assert "log_alpha is not 16-byte aligned" in lib.kda_last_error().decode()
+
+
+@pytest.mark.parametrize("B,T,H,N", [(1, 300, 70000, 1), (65536, 300, 4, 65536), (60000, 60000, 4, 60000)])
+def test_sizes_that_are_refused_need_nothing(lib, B, T, H, N):  # noqa: F811
+    """A caller that allocates first gets the refusal, not an allocation that cannot be had."""
+    for slots in (0, 1):
+        assert lib.kda_la_chunk_forward_workspace_size(B, T, H, 128, 128, N, 0, slots) == 0
+    assert lib.kda_la_chunk_backward_workspace_size(B, T, H, 128, 128, N, 0) == 0
+    assert abi.prefill(lib, B=B, T=T, H=H, N=N, ws=None, wsb=0) == abi.UNSUPPORTED
+    assert abi.slots(lib, B=B, T=T, H=H, N=N, ws=None, wsb=0) == abi.UNSUPPORTED
+    assert abi.backward(lib, B=B, T=T, H=H, N=N, ws=None, wsb=0) == abi.UNSUPPORTED
