@@ -14,7 +14,8 @@ Attention の仕組み"), per (sequence, head), with a dk x dv fp32 state S:
     S' = Diag(exp(log_alpha_t)) S;  S = S' + beta_t k_t (v_t - S'^T k_t)^T;  o_t = S^T q_t
 
 Linear attention with a constant decay for each head (la_*: S = exp(log_decay_h) S + k_t v_t^T)
-shares its layouts, states and slots; group_norm is the norm behind either kind of layer.
+shares its layouts, states and slots; group_norm is the norm behind such layers' heads (it takes
+the mean out: KDA and Gated DeltaNet layers have an RMS norm there, which it is not).
 """
 from __future__ import annotations
 

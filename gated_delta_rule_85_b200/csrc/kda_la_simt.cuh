@@ -5,9 +5,10 @@
 // of a 16 x 16 grid holds DAB/16 rows x DC/16 columns) and is put in shared memory
 // once a chunk for the product with the a rows.
 //
-// Bound by shared-memory reads (a 16-byte read is four wavefronts, whoever shares it): 2 x 1003
-// tokens x 8 heads of 64 x 128 take 65 us, of which the walk 42 in spans of one and two chunks
-// (64 of 128 columns a CTA, two CTAs an SM: 50; 512 threads of two token rows: 55).
+// Bound by latency with one CTA of 8 warps an SM and by its shared-memory reads (a 16-byte read is four
+// wavefronts, whoever shares it; 40 % of the cycles): 2 x 1003 tokens x 8 heads of 64 x 128 take 65 us, of which the
+// walk 42 in spans of one and two chunks (64 of 128 columns a CTA, two CTAs an SM: 50; 512 threads of two token rows:
+// 55); its gradients take 164.
 #pragma once
 
 #include "kda_la.cuh"
@@ -284,6 +285,10 @@ struct Call {
 //   bf16 forward   2 x 300 x 32 heads of 128 39 | 25;  8 x 2048 x 32 222 | 165;  4 x 1000 x 8 37 | 47
 //   bf16 gradients 4 x 1000 x 8 heads of 128 75 | 48;  8 x 2048 x 32 532 | 402;  1 x 1500 x 4 29 | 63
 //   fp32 forward   8 x 500 x 16 heads of 64 164 | 91;  1 x 200 x 8 44 | 94
+// and behind them, where the rule takes the slower side: gradients of 2 x 2000 x 16 heads of 64 x 128 92 | 121 (whole;
+// two launches of walks there, the model counts one) and of 4 x 2048 x 16 heads of 128 172 | 150 (cut); fp32 2 x 500 x
+// 40 heads of 64 130 | 100 forward, 370 | 317 gradients (cut).  In 38 other measurements it takes the faster one, heads of
+// 64, of 128 and mixed in either type.
 template <int C>
 Geo geo_of(const Call &c, int walks, int sums, bool side_by_side) {
     Geo g{c.cu, c.T, c.N, c.H, 0, 0, 0, 0, 1};

@@ -513,7 +513,8 @@ int kda_la_chunk_backward(const void *q, const void *k, const void *v, const flo
 /*
  * Group norm with an activation, channels last: the norm between such a layer's
  * heads and its output projection (one group per head: x = o as [B T, 1, H dv],
- * G = H), or of any [N, L, C] tensor.
+ * G = H), or of any [N, L, C] tensor.  The mean is taken out: it is not the RMS norm that
+ * KDA and Gated DeltaNet layers have in that place.
  *
  *     xhat = (x - mean) / sqrt(var + eps)     over the L positions and C / G channels of a group
  *     z = xhat weight + bias;   y = act(z), or z act(gate) with a gate
