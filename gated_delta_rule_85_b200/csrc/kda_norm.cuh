@@ -1194,7 +1194,7 @@ inline long long gcd_of(long long a, long long b) { return b ? gcd_of(b, a % b) 
 // Forward the cluster wins or is equal in all of 22 sizes of 13 thousand to 4 million elements.  The gradients' border lies
 // between 1.2 and 4 million and no count of elements draws it exactly.  Positions are taken at 3 x 2048 x 320 14.5 | 16.4,
 // 64 x 128 x 320 18.5 | 20.5, 512 x 16 x 256 20.5 | 22.6, fp32 4 x 1024 x 512 14.4 | 16.4 and 1 x 4096 x 512 12.3 | 18.5, and
-// the cluster at fp32 with a gate 2 x 1021 x 640 18.5 | 16.5; in the 16 other sizes measured the rule takes the faster one.
+// the cluster at fp32 with a gate 2 x 1021 x 640 18.5 | 16.5; in the 16 other sizes measured it takes the faster one or one within 4 %.
 constexpr size_t kClusterWant = 56 * 1024, kClusterSmem = 200 * 1024;
 constexpr long long kClusterGrad = 3 << 19;
 inline bool cluster_plan(long long N, int L, int C, int G, int esize, bool gated, bool backward, Plan &s) {
